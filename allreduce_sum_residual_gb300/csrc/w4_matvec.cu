@@ -1,0 +1,167 @@
+// ar_w4_matvec and ar_w4_matvec_experts: checks, the launch shape, and the
+// dense kernels (w4_matvec.cuh; the experts' are in w4_experts.cu).
+#include <mutex>
+
+#include "w4_matvec.cuh"
+
+namespace arn {
+
+W4Kernel w4_dense_kernel(int r, int nt, int group) { return w4_pick<false>(r, nt, group); }
+
+// Every kernel may use all of an SM's shared memory; set once per device by
+// the first call, which must be outside graph capture (as for the rest of
+// the library).
+static int allow_shared_memory(int bytes) {
+  static std::mutex mu;
+  static bool done[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return AR_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return AR_OK;
+  for (int r = 1; r <= 4; r *= 2)
+    for (int nt = 1; nt <= 2; ++nt)
+      for (int group = 32; group <= 128; group *= 2)
+        for (int e = 0; e < 2; ++e) {
+          const W4Kernel kern = e ? w4_experts_kernel(r, nt, group) : w4_dense_kernel(r, nt, group);
+          if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return AR_ERR_CUDA;
+          }
+        }
+  done[dev] = true;
+  return AR_OK;
+}
+
+struct W4Plan {
+  int r, nt, split, cols, ctas_per_sm;
+};
+
+// Lays out shared memory for a plan; its bytes.
+static int64_t w4_layout(const W4Plan &p, int group, int units, int pairs, bool experts, W4Args *a) {
+  const int depth = p.r == 1 ? w4_depth<1>() : p.r == 2 ? w4_depth<2>() : w4_depth<4>();
+  int64_t at = int64_t{kW4Warps} * depth * 16 * p.r * w4_row_bytes(group);
+  a->xs_offset = static_cast<int>(at);
+  at += int64_t{(units + p.split - 1) / p.split} * 256 * p.cols;
+  a->red_offset = static_cast<int>(at);
+  at += int64_t{kW4Warps} * p.cols * 16 * p.r * 4;
+  a->part_offset = static_cast<int>(at);
+  if (p.split > 1) at += int64_t{2} * p.cols * 16 * p.r * 4;
+  a->ids_offset = static_cast<int>(at);
+  if (experts) at += (int64_t{2} * pairs + 15) / 16 * 16;
+  a->smem_bytes = static_cast<int>(at);
+  return at;
+}
+
+static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k, const void *q,
+                  const void *scales, int scales_type, const void *zeros, int E, int64_t N, int64_t K,
+                  int group, int act, void *out, bool experts, void *stream) {
+  const int size = type_size(scales_type);
+  if (m < 0 || k < 1 || E < 1 || N < 1 || K < 1 || size == 0 ||
+      (group != 32 && group != 64 && group != 128) || (act != AR_ACT_NONE && act != AR_ACT_SILU_MUL) ||
+      (x_per_pair != 0 && x_per_pair != 1))
+    return AR_ERR_ARG;
+  if (K % group != 0 || (act == AR_ACT_SILU_MUL && N % 2 != 0)) return AR_ERR_ARG;
+  if (E > AR_MAX_EXPERTS || k > AR_MAX_TOPK || K > AR_MATVEC_MAX_K || N > AR_MATVEC_MAX_N ||
+      m > (experts ? AR_MATVEC_MAX_PAIRS / k : AR_MATVEC_MAX_ROWS))
+    return AR_ERR_UNSUPPORTED;
+  if (m == 0) return AR_OK;
+  if (!x || !q || !scales || !out || (experts && !ids)) return AR_ERR_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned16(zeros) ||
+      !aligned_to(out, 2) || !aligned_to(ids, 4))
+    return AR_ERR_ALIGN;
+  const int64_t pairs = m * k, ng = K / group;
+  const int64_t width = act == AR_ACT_SILU_MUL ? N / 2 : N;
+  const Range o = range_of(out, pairs * width * 2);
+  if (overlap(o, range_of(x, (x_per_pair ? pairs : m) * K * 2)) ||
+      overlap(o, range_of(ids, ids ? pairs * 4 : 0)) || overlap(o, range_of(q, E * N * (K / 2))) ||
+      overlap(o, range_of(scales, E * N * ng * size)) ||
+      overlap(o, range_of(zeros, zeros ? E * N * ng : 0)))
+    return AR_ERR_ALIAS;
+  int st;
+  DeviceState *d = current_device(&st);
+  if (!d) return st;
+  // Dynamic shared memory beside the kernels' own (the experts' tables).
+  const int64_t most = d->smem_optin - 4096;
+  st = allow_shared_memory(static_cast<int>(most));
+  if (st != AR_OK) return st;
+  W4Args a = {};
+  a.x = static_cast<const uint4 *>(x);
+  a.ids = ids;
+  a.q = static_cast<const uint8_t *>(q);
+  a.scales = static_cast<const uint8_t *>(scales);
+  a.zeros = static_cast<const uint8_t *>(zeros);
+  a.out = static_cast<__nv_bfloat16 *>(out);
+  a.scale_bytes = E * N * ng * size;
+  a.zero_bytes = E * N * ng;
+  a.pairs = static_cast<int>(pairs);
+  a.k = x_per_pair ? 1 : k;
+  a.E = E;
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.ng = static_cast<int>(ng);
+  a.width = static_cast<int>(width);
+  a.act = act;
+  a.scale_type = scales_type;
+  a.units = static_cast<int>((K + kW4UnitK - 1) / kW4UnitK);
+  a.status = d->status;
+
+  W4Plan p;
+  p.nt = m <= 8 ? 1 : 2;
+  p.cols = static_cast<int>(pairs < 8 * p.nt ? pairs : 8 * p.nt);
+  // Most column sets: each has an expert of its own or is full.
+  int64_t sets = experts ? E + pairs / p.cols : (pairs + p.cols - 1) / p.cols;
+  if (sets > pairs) sets = pairs;
+  // Tall items where there are plenty, so that x is read from shared memory
+  // once per 64 rows; short ones where they have to spread over the SMs.
+  p.r = 4;
+  while (p.r > 1 && sets * ((N + 16 * p.r - 1) / (16 * p.r)) < 4 * d->sms) p.r /= 2;
+  for (;; p.r /= 2) {
+    // One-tile items leave room for a second CTA on the SM.
+    const int64_t room = p.r == 1 ? most / 2 : most;
+    p.split = 1;
+    while (p.split < 8 && w4_layout(p, group, a.units, a.pairs, experts, &a) > room) p.split *= 2;
+    if (p.r == 1 || w4_layout(p, group, a.units, a.pairs, experts, &a) <= room) break;
+  }
+  if (w4_layout(p, group, a.units, a.pairs, experts, &a) > most) return AR_ERR_UNSUPPORTED;
+  p.ctas_per_sm = a.smem_bytes <= most / 2 ? 2 : 1;
+  a.cols = p.cols;
+  a.split = p.split;
+  const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
+  a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
+  int64_t clusters = sets * a.row_blocks;
+  const int64_t cap = int64_t{d->sms} * p.ctas_per_sm / p.split;
+  if (clusters > cap) clusters = cap;
+  const W4Kernel kern =
+      experts ? w4_experts_kernel(p.r, p.nt, group) : w4_dense_kernel(p.r, p.nt, group);
+  return launch_pdl(kern, a, clusters * p.split, kW4Threads, static_cast<size_t>(a.smem_bytes),
+                    p.split, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? AR_OK
+             : AR_ERR_CUDA;
+}
+
+}  // namespace arn
+
+using namespace arn;
+
+extern "C" {
+
+int ar_w4_matvec(const void *x, const void *q, const void *scales, int scales_type,
+                 const void *zeros, int64_t m, int64_t N, int64_t K, int group, int act, void *out,
+                 void *stream) {
+  return run_w4(x, 0, nullptr, m, 1, q, scales, scales_type, zeros, 1, N, K, group, act, out, false,
+                stream);
+}
+
+int ar_w4_matvec_experts(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k,
+                         const void *q, const void *scales, int scales_type, const void *zeros,
+                         int E, int64_t N, int64_t K, int group, int act, void *out, void *stream) {
+  return run_w4(x, x_per_pair, ids, m, k, q, scales, scales_type, zeros, E, N, K, group, act, out,
+                true, stream);
+}
+
+}  // extern "C"

@@ -356,6 +356,164 @@ int ar_rmsnorm_two_stage_static(const void *const *partials, int n,
                                 void *residual_out, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * The expert layer: what a mixture-of-experts decoder layer computes between
+ * two epilogues.  ar_route_experts picks each token's experts from its
+ * logits, ar_w4_matvec_experts (and ar_w4_matvec, for dense projections)
+ * multiply by 4-bit weights at decode batch sizes, and ar_combine sums the
+ * chosen experts' rows -- into the rank's partial that ar_rmsnorm reduces,
+ * or, in ar_combine_rmsnorm, straight through the residual add and RMSNorm.
+ *
+ * Streams, graph capture and ownership are those of the epilogue calls: the
+ * calls are asynchronous, allocate nothing and keep no state, so calls on
+ * different streams may overlap.  Device memory of the current device,
+ * row-major.  No output may overlap an input or another output
+ * (AR_ERR_ALIAS), but residual_out may be residual.  m == 0 is a no-op that
+ * checks only the sizes and the options.
+ * --------------------------------------------------------------------------- */
+
+/* Element types of the arrays that are not always bf16. */
+#define AR_TYPE_F32  0
+#define AR_TYPE_BF16 1
+#define AR_TYPE_F16  2
+
+/* Scores of ar_route_experts. */
+#define AR_SCORE_SOFTMAX 0
+#define AR_SCORE_SIGMOID 1
+
+/* Scores of a group of experts. */
+#define AR_GROUP_MAX  0   /* its largest choice                               */
+#define AR_GROUP_TOP2 1   /* the sum of its two largest choices               */
+
+/* What follows a 4-bit product. */
+#define AR_ACT_NONE     0
+#define AR_ACT_SILU_MUL 1 /* rows [0, N/2) gate rows [N/2, N): out =
+                             gate / (1 + exp(-gate)) * up, N/2 columns        */
+
+#define AR_MAX_EXPERTS      512   /* experts of one layer                     */
+#define AR_MAX_TOPK         16    /* experts of one token                     */
+#define AR_MATVEC_MAX_ROWS  64    /* rows of ar_w4_matvec                     */
+#define AR_MATVEC_MAX_PAIRS 4096  /* m * k of ar_w4_matvec_experts            */
+#define AR_MATVEC_MAX_K     32768 /* longest dot product of the 4-bit calls   */
+#define AR_MATVEC_MAX_N     1048576 /* rows of one 4-bit matrix               */
+
+/*
+ * Route every token to k experts.  For a row x of E logits:
+ *   score   s_e = exp(x_e) / sum exp(x)  or  1 / (1 + exp(-x_e))
+ *   choice  c_e = s_e + bias_e (without a bias the choices rank as the
+ *           logits do)
+ *   groups  the E experts are `groups` runs of E/groups; a group's score is
+ *           its largest choice or the sum of its two largest, and only the
+ *           experts of the topk_groups best groups can be chosen
+ *   ids     the k largest choices, largest first
+ *   weights s of the chosen (the bias only steers the choice); with renorm
+ *           divided by their sum (0 where that is 0); times `scale`.
+ * Equal choices, and equal groups, go to the lowest index; "equal" and
+ * "larger" are decided as 64-bit arithmetic decides them, so ids do not
+ * depend on the launch shape.  A logit of -inf is an expert that is off: its
+ * score is 0 and it ranks, like one with a NaN choice, below every other
+ * expert of the kept groups, lowest index first; a group's score is -inf
+ * where it has too few experts that are on.  A row with nothing on gets the
+ * lowest indices and weights of 0.  ids are always k distinct values in
+ * [0, E).  NaN logits, and +inf under softmax, give NaN weights.  The pages
+ * have no counterpart of it.
+ *   logits       [m, E] of logits_type, row r at logits + r * row_stride
+ *                elements (row_stride >= E); aligned to its element.
+ *   bias         [E] fp32, or NULL.
+ *   E            1 .. AR_MAX_EXPERTS, a multiple of `groups` (1 .. 32).
+ *   topk_groups  1 .. groups.
+ *   group_score  AR_GROUP_MAX or AR_GROUP_TOP2 (groups of two or more);
+ *                without effect with one group.
+ *   k            1 .. AR_MAX_TOPK, at most topk_groups * E/groups.
+ *   weights      [m, k] fp32.     ids  [m, k] int32.
+ * AR_ERR_ARG for anything outside these, AR_ERR_UNSUPPORTED for E or k above
+ * the limits.
+ */
+int ar_route_experts(const void *logits, int logits_type, int64_t row_stride,
+                     const float *bias, int64_t m, int E, int k, int scoring,
+                     int groups, int topk_groups, int group_score, int renorm,
+                     float scale, float *weights, int32_t *ids, void *stream);
+
+/*
+ * out[i, n] = bf16( sum_k x[i, k] W[n, k] ),  or its gated half (act), with
+ *   W[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
+ * for a decode batch of m rows: the weights are read once per 16 rows, at
+ * the speed of memory.  Products are summed in fp32; s multiplies the fp32
+ * sum of its group; one rounding, at the end.  The pages have no counterpart
+ * of it.
+ *   x        [m, K] bf16.  m <= AR_MATVEC_MAX_ROWS.
+ *   q        [N, K/2] bytes, two weights each: the low four bits hold the
+ *            even k.
+ *   scales   [N, K/group] of scales_type.
+ *   zeros    [N, K/group] bytes (the low four bits count), or NULL: z = 8.
+ *   group    32, 64 or 128; K a multiple of it, K <= AR_MATVEC_MAX_K.
+ *   N        1 .. AR_MATVEC_MAX_N; even with AR_ACT_SILU_MUL.
+ *   act      AR_ACT_NONE or AR_ACT_SILU_MUL.
+ *   out      [m, N] bf16, or [m, N/2] with AR_ACT_SILU_MUL.
+ * x, q, scales and zeros must be 16-byte aligned, out 2-byte.  AR_ERR_ARG,
+ * AR_ERR_ALIGN, AR_ERR_UNSUPPORTED (m, N or K above the limits) or
+ * AR_ERR_ALIAS.
+ */
+int ar_w4_matvec(const void *x, const void *q, const void *scales,
+                 int scales_type, const void *zeros, int64_t m, int64_t N,
+                 int64_t K, int group, int act, void *out, void *stream);
+
+/*
+ * ar_w4_matvec with the weights of the routed experts:
+ *   out[i, j, :] = x_ij * W[ids[i, j]]^T
+ * An expert's weights are read once for all its tokens (per 16 of them).
+ * The pages have no counterpart of it.
+ *   x            [m, K] bf16 with x_per_pair = 0 (every choice of a token
+ *                takes the token's row), [m, k, K] with x_per_pair = 1.
+ *   ids          [m, k] int32.  A value outside [0, E) is an expert that is
+ *                not here (another rank's): its row of out is zero.  A token
+ *                may name an expert twice.
+ *   q, scales, zeros  as in ar_w4_matvec with a leading dimension E.
+ *   m * k        at most AR_MATVEC_MAX_PAIRS; k <= AR_MAX_TOPK; E <=
+ *                AR_MAX_EXPERTS.
+ *   out          [m, k, N] bf16 ([m, k, N/2] with AR_ACT_SILU_MUL).
+ * ids must be 4-byte aligned.  Otherwise as ar_w4_matvec.
+ */
+int ar_w4_matvec_experts(const void *x, int x_per_pair, const int32_t *ids,
+                         int64_t m, int k, const void *q, const void *scales,
+                         int scales_type, const void *zeros, int E, int64_t N,
+                         int64_t K, int group, int act, void *out,
+                         void *stream);
+
+/*
+ * The weighted sum of each token's expert outputs, as a partial:
+ *   out[i, :] = bf16( shared[i, :] + sum_j weights[i, j] y[slot_ij, :] )
+ * in fp32, j in order.  slot_ij = slots[i, j], or i * k + j without slots; a
+ * slot outside [0, rows) adds nothing, whatever its weight (a choice that
+ * another rank computed).  A token without a live slot gets shared's row, or
+ * zeros.  `out` may be a buffer of ar_rmsnorm's partials.  The pages have no
+ * counterpart of it.
+ *   y        [rows, H] bf16 (without slots rows must be m * k).
+ *   slots    [m, k] int32, or NULL.      weights  [m, k] fp32.
+ *   shared   [m, H] bf16, or NULL.       out      [m, H] bf16.
+ *   k        1 .. AR_MAX_TOPK.           H        as in ar_rmsnorm.
+ * Every bf16 array must be 16-byte aligned, slots and weights 4-byte.
+ */
+int ar_combine(const void *y, int64_t rows, const int32_t *slots,
+               const float *weights, const void *shared, int64_t m, int k,
+               int64_t H, void *out, void *stream);
+
+/*
+ * ar_combine's sum, unrounded, through ar_rmsnorm's residual add and RMSNorm
+ * in the same pass:
+ *   r = shared + sum_j weights_j y[slot_j] + residual          fp32
+ *   residual_out = bf16(r)
+ *   out          = bf16(r * rsqrt(mean(r^2) + eps) * weight)
+ * residual, weight, eps, out and residual_out as in ar_rmsnorm, the rest as
+ * in ar_combine.  For one rank; with several, ar_combine's partial goes
+ * through ar_rmsnorm.  The pages have no counterpart of it.
+ */
+int ar_combine_rmsnorm(const void *y, int64_t rows, const int32_t *slots,
+                       const float *weights, const void *shared,
+                       const void *residual, const void *weight, float eps,
+                       int64_t m, int k, int64_t H, void *out,
+                       void *residual_out, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Cross-rank data plane: what the all-reduce needs when the n partials are
  * the buffers of n processes (one per GPU, or several on one GPU).
  *
