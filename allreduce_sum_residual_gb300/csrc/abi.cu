@@ -759,7 +759,7 @@ const char *ar_strerror(int status) {
     case AR_ERR_WORKSPACE: return "two-stage workspace missing or too small: call ar_reserve_workspace";
     case AR_ERR_CUDA: return "CUDA runtime error or launch failure";
     case AR_ERR_TIMEOUT: return "a bounded device-side wait timed out";
-    case AR_ERR_UNSUPPORTED: return "unsupported size (H above AR_MAX_HIDDEN or too many rows)";
+    case AR_ERR_UNSUPPORTED: return "unsupported size (H above AR_MAX_HIDDEN, too many rows, or an expert-layer limit)";
     case AR_ERR_BOUNDS: return "a device-side bounds check failed (checking build)";
     case AR_ERR_SCRATCH_LIMIT:
       return "m*H exceeds the fixed device scratch of ar_rmsnorm_two_stage_static (AR_STATIC_SCRATCH_ELEMS)";

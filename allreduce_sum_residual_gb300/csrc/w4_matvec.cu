@@ -39,6 +39,7 @@ static int allow_shared_memory(int bytes) {
 
 struct W4Plan {
   int r, nt, split, cols, ctas_per_sm;
+  int64_t sets;  // most column sets
 };
 
 // Lays out shared memory for a plan; its bytes.
@@ -55,6 +56,31 @@ static int64_t w4_layout(const W4Plan &p, int group, int units, int pairs, bool 
   if (experts) at += (int64_t{2} * pairs + 15) / 16 * 16;
   a->smem_bytes = static_cast<int>(at);
   return at;
+}
+
+// Columns: the batch, up to 16; tall items where there are plenty, so that x
+// is read from shared memory once per 64 rows, short ones where they have to
+// spread over the SMs; then the fewest CTAs per item whose slices of x fit
+// beside the rings.  Where nothing fits (the longest rows), fewer columns at
+// a time.  Leaves the layout in *a.
+static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
+                    W4Plan *p) {
+  for (p->nt = m <= 8 ? 1 : 2; p->nt >= 1; --p->nt) {
+    p->cols = a->pairs < 8 * p->nt ? a->pairs : 8 * p->nt;
+    // Each set has an expert of its own or is full.
+    p->sets = experts ? a->E + a->pairs / p->cols : (a->pairs + p->cols - 1) / p->cols;
+    if (p->sets > a->pairs) p->sets = a->pairs;
+    for (p->r = 4; p->r >= 1; p->r /= 2) {
+      if (p->r > 1 && p->sets * ((a->N + 16 * p->r - 1) / (16 * p->r)) < 4 * sms) continue;
+      for (p->split = 1; p->split <= 8; p->split *= 2) {
+        const int64_t bytes = w4_layout(*p, group, a->units, a->pairs, experts, a);
+        if (bytes > most) continue;
+        p->ctas_per_sm = bytes <= most / 2 ? 2 : 1;
+        return true;
+      }
+    }
+  }
+  return false;
 }
 
 static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k, const void *q,
@@ -111,29 +137,12 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.status = d->status;
 
   W4Plan p;
-  p.nt = m <= 8 ? 1 : 2;
-  p.cols = static_cast<int>(pairs < 8 * p.nt ? pairs : 8 * p.nt);
-  // Most column sets: each has an expert of its own or is full.
-  int64_t sets = experts ? E + pairs / p.cols : (pairs + p.cols - 1) / p.cols;
-  if (sets > pairs) sets = pairs;
-  // Tall items where there are plenty, so that x is read from shared memory
-  // once per 64 rows; short ones where they have to spread over the SMs.
-  p.r = 4;
-  while (p.r > 1 && sets * ((N + 16 * p.r - 1) / (16 * p.r)) < 4 * d->sms) p.r /= 2;
-  for (;; p.r /= 2) {
-    // One-tile items leave room for a second CTA on the SM.
-    const int64_t room = p.r == 1 ? most / 2 : most;
-    p.split = 1;
-    while (p.split < 8 && w4_layout(p, group, a.units, a.pairs, experts, &a) > room) p.split *= 2;
-    if (p.r == 1 || w4_layout(p, group, a.units, a.pairs, experts, &a) <= room) break;
-  }
-  if (w4_layout(p, group, a.units, a.pairs, experts, &a) > most) return AR_ERR_UNSUPPORTED;
-  p.ctas_per_sm = a.smem_bytes <= most / 2 ? 2 : 1;
+  if (!w4_plan(m, experts, group, most, d->sms, &a, &p)) return AR_ERR_UNSUPPORTED;
   a.cols = p.cols;
   a.split = p.split;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
   a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
-  int64_t clusters = sets * a.row_blocks;
+  int64_t clusters = p.sets * a.row_blocks;
   const int64_t cap = int64_t{d->sms} * p.ctas_per_sm / p.split;
   if (clusters > cap) clusters = cap;
   const W4Kernel kern =
