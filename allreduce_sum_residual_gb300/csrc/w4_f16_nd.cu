@@ -1,0 +1,11 @@
+// The 4-bit products' kernels (w4_matvec.cuh) with f16 scales, no zero points,
+// one matrix: apart from the others so that they compile in parallel.
+#include "w4_matvec.cuh"
+
+namespace arn {
+
+W4Kernel w4_kernel_f16_nd(int r, int nt, int group) {
+  return w4_pick_tile<AR_TYPE_F16, false, false>(r, nt, group);
+}
+
+}  // namespace arn

@@ -1,12 +1,34 @@
-// ar_w4_matvec and ar_w4_matvec_experts: checks, the launch shape, and the
-// dense kernels (w4_matvec.cuh; the experts' are in w4_experts.cu).
+// ar_w4_matvec and ar_w4_matvec_experts: checks and the launch shape.  The
+// kernels (w4_matvec.cuh) are compiled in w4_<scale type>_<zero points: z or
+// n><experts: e or d>.cu.
 #include <mutex>
 
 #include "w4_matvec.cuh"
 
 namespace arn {
 
-W4Kernel w4_dense_kernel(int r, int nt, int group) { return w4_pick<false>(r, nt, group); }
+// Row tiles 1 or 2, column tiles 1 or 2, groups of 32, 64 or 128.
+W4Kernel w4_kernel_f32_nd(int r, int nt, int group);
+W4Kernel w4_kernel_f32_ne(int r, int nt, int group);
+W4Kernel w4_kernel_f32_zd(int r, int nt, int group);
+W4Kernel w4_kernel_f32_ze(int r, int nt, int group);
+W4Kernel w4_kernel_bf16_nd(int r, int nt, int group);
+W4Kernel w4_kernel_bf16_ne(int r, int nt, int group);
+W4Kernel w4_kernel_bf16_zd(int r, int nt, int group);
+W4Kernel w4_kernel_bf16_ze(int r, int nt, int group);
+W4Kernel w4_kernel_f16_nd(int r, int nt, int group);
+W4Kernel w4_kernel_f16_ne(int r, int nt, int group);
+W4Kernel w4_kernel_f16_zd(int r, int nt, int group);
+W4Kernel w4_kernel_f16_ze(int r, int nt, int group);
+
+static W4Kernel w4_kernel(int type, bool zeros, bool experts, int r, int nt, int group) {
+  using Pick = W4Kernel (*)(int, int, int);
+  static const Pick picks[3][2][2] = {
+      {{w4_kernel_f32_nd, w4_kernel_f32_ne}, {w4_kernel_f32_zd, w4_kernel_f32_ze}},
+      {{w4_kernel_bf16_nd, w4_kernel_bf16_ne}, {w4_kernel_bf16_zd, w4_kernel_bf16_ze}},
+      {{w4_kernel_f16_nd, w4_kernel_f16_ne}, {w4_kernel_f16_zd, w4_kernel_f16_ze}}};
+  return picks[type][zeros ? 1 : 0][experts ? 1 : 0](r, nt, group);
+}
 
 // Every kernel may use all of an SM's shared memory; set once per device by
 // the first call, which must be outside graph capture (as for the rest of
@@ -21,48 +43,42 @@ static int allow_shared_memory(int bytes) {
   }
   std::lock_guard<std::mutex> lock(mu);
   if (done[dev]) return AR_OK;
-  for (int r = 1; r <= 4; r *= 2)
-    for (int nt = 1; nt <= 2; ++nt)
-      for (int group = 32; group <= 128; group *= 2)
-        for (int e = 0; e < 2; ++e) {
-          const W4Kernel kern = e ? w4_experts_kernel(r, nt, group) : w4_dense_kernel(r, nt, group);
-          if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   bytes) != cudaSuccess) {
-            cudaGetLastError();
-            return AR_ERR_CUDA;
-          }
+  for (int type = AR_TYPE_F32; type <= AR_TYPE_F16; ++type)
+    for (int i = 0; i < 16; ++i)
+      for (int group = 32; group <= 128; group *= 2) {
+        const W4Kernel kern = w4_kernel(type, i & 1, i & 2, i & 4 ? 2 : 1, i & 8 ? 2 : 1, group);
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 bytes) != cudaSuccess) {
+          cudaGetLastError();
+          return AR_ERR_CUDA;
         }
+      }
   done[dev] = true;
   return AR_OK;
 }
 
 struct W4Plan {
-  int r, nt, split, cols, ctas_per_sm;
+  int r, nt, warps, team, split, cols, ctas_per_sm;
   int64_t sets;  // most column sets
 };
 
 // Lays out shared memory for a plan; its bytes.
 static int64_t w4_layout(const W4Plan &p, int group, int units, int pairs, bool experts, W4Args *a) {
-  const int depth = p.r == 1 ? w4_depth<1>() : p.r == 2 ? w4_depth<2>() : w4_depth<4>();
-  int64_t at = int64_t{kW4Warps} * depth * 16 * p.r * w4_row_bytes(group);
+  const int64_t slice = (units + p.split - 1) / p.split;  // a CTA's units of an item
+  int64_t at = int64_t{p.warps} * w4_depth(p.r) * w4_slot_bytes(p.r, group);
   a->xs_offset = static_cast<int>(at);
-  at += int64_t{(units + p.split - 1) / p.split} * 256 * p.cols;
+  at += slice * 256 * p.cols;
+  a->sum_offset = static_cast<int>(at);
+  at += slice * (kW4UnitK / group) * 8 * p.nt * 4;
   a->red_offset = static_cast<int>(at);
-  at += int64_t{kW4Warps} * p.cols * 16 * p.r * 4;
-  a->part_offset = static_cast<int>(at);
-  if (p.split > 1) at += int64_t{2} * p.cols * 16 * p.r * 4;
+  if (p.team > 1 || p.split > 1) at += int64_t{2} * p.warps * p.cols * 16 * p.r * 4;
   a->ids_offset = static_cast<int>(at);
   if (experts) at += (int64_t{2} * pairs + 15) / 16 * 16;
   a->smem_bytes = static_cast<int>(at);
   return at;
 }
 
-// Columns: the batch, up to 16; tall items where there are plenty, so that x
-// is read from shared memory once per 64 rows, short ones where they have to
-// spread over the SMs; then the fewest CTAs per item whose slices of x fit
-// beside the rings.  Where nothing fits (the longest rows), fewer columns at
-// a time.  Leaves the layout in *a.
 static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
                     W4Plan *p) {
   for (p->nt = m <= 8 ? 1 : 2; p->nt >= 1; --p->nt) {
@@ -70,14 +86,18 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
     // Each set has an expert of its own or is full.
     p->sets = experts ? a->E + a->pairs / p->cols : (a->pairs + p->cols - 1) / p->cols;
     if (p->sets > a->pairs) p->sets = a->pairs;
-    for (p->r = 4; p->r >= 1; p->r /= 2) {
+    for (p->r = 2; p->r >= 1; p->r /= 2) {
       if (p->r > 1 && p->sets * ((a->N + 16 * p->r - 1) / (16 * p->r)) < 4 * sms) continue;
-      for (p->split = 1; p->split <= 8; p->split *= 2) {
-        const int64_t bytes = w4_layout(*p, group, a->units, a->pairs, experts, a);
-        if (bytes > most) continue;
-        p->ctas_per_sm = bytes <= most / 2 ? 2 : 1;
-        return true;
-      }
+      for (p->warps = 16; p->warps >= 8; p->warps /= 2)
+        for (p->split = 1; p->split <= 8 && p->split <= a->units; p->split *= 2) {
+          const int slice = (a->units + p->split - 1) / p->split;
+          p->team = 1;
+          while (p->team < p->warps && slice >= 4 * p->team) p->team *= 2;
+          const int64_t bytes = w4_layout(*p, group, a->units, a->pairs, experts, a);
+          if (bytes > most) continue;
+          p->ctas_per_sm = 1;
+          return true;
+        }
     }
   }
   return false;
@@ -140,14 +160,14 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   if (!w4_plan(m, experts, group, most, d->sms, &a, &p)) return AR_ERR_UNSUPPORTED;
   a.cols = p.cols;
   a.split = p.split;
+  a.team = p.team;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
   a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
   int64_t clusters = p.sets * a.row_blocks;
   const int64_t cap = int64_t{d->sms} * p.ctas_per_sm / p.split;
   if (clusters > cap) clusters = cap;
-  const W4Kernel kern =
-      experts ? w4_experts_kernel(p.r, p.nt, group) : w4_dense_kernel(p.r, p.nt, group);
-  return launch_pdl(kern, a, clusters * p.split, kW4Threads, static_cast<size_t>(a.smem_bytes),
+  const W4Kernel kern = w4_kernel(scales_type, zeros != nullptr, experts, p.r, p.nt, group);
+  return launch_pdl(kern, a, clusters * p.split, p.warps * 32, static_cast<size_t>(a.smem_bytes),
                     p.split, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? AR_OK
              : AR_ERR_CUDA;

@@ -13,27 +13,32 @@
 // the bytes that came in; its rate is of no use to a kernel that reads each
 // weight once.)
 //
-// Exactness.  q - z is an integer in [-15, 15], exact in bf16: the four bits
-// under the exponent of 128 are the number 128 + q, and 128 + z is
-// subtracted from it.  The tensor core sums a group's products in fp32, the
-// group's scale multiplies that sum in fp32, and the groups are added in
-// fp32: first a warp's, then the warps' in order, then the CTAs' in order.
+// Exactness.  The four bits of a weight under the exponent of 16 are the
+// number 16 + q, exact in bf16; a pair costs a shift and one logic operation.
+// The tensor core sums a group's (16 + q) x in fp32, (16 + z) times the
+// group's sum of x (fp32, made once per column set) comes off it, the scale
+// multiplies it in fp32, and the groups are added in fp32: a warp's, then
+// the warps' in order, CTA by CTA.  (Subtracting the zero point from every
+// pair instead would cost three instructions in eleven; the offset makes the
+// running sum about five times larger, two of fp32's 24 bits, far below the
+// bf16 result.)
 //
 // Layout.  The weights are read as they are stored.  A warp takes units of
 // 16 R rows x 128 k (64 bytes a row) into its own ring of shared memory with
-// 16-byte asynchronous copies; nothing but the warp waits for it.  Rows lie
-// 80 bytes apart (112 with groups of 32), so that the 32 words of an operand
-// load fall into 32 banks; the bytes between hold the unit's scales and zero
-// points.  Word t of a 16-byte piece of row g is lane (g, t)'s: its eight
-// weights are two pairs for each of two products.  The pairs of a word come
-// out as (i, i + 4), so x is stored with its eights in that order, once per
-// column set.  Within one product all k belong to the same 32, so that every
-// group size can be scaled after it.
+// 16-byte asynchronous copies; nothing but the warp waits for it.  A lane
+// (g, t) reads the words t, t + 4, ... of row g with groups of 32, so that
+// all k of one product lie in one 32, two neighbouring words of each 64 with
+// groups of 64, and four neighbouring words with groups of 128: one wide
+// load where the group allows it.  The row stride (112, 96, 64 bytes) keeps
+// each of these free of bank conflicts.  The pairs of a word come out as
+// (i, i + 4), so x is stored with its eights in that order, in the order of
+// the lanes.
 //
 // Work.  An item is 16 R rows x one column set (an expert's tokens, up to
 // 8 NT).  A cluster of S CTAs takes a contiguous range of items, CTA q of it
-// the units q, q + S, ... of each; the warps of a CTA take its units in
-// turn.  The ring runs on across items.
+// the units q, q + S, ... of each.  A CTA's warps form teams: a team takes
+// items of the range in turn, and its warps the units of an item in turn.
+// The ring runs on across items.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,8 +47,7 @@
 
 namespace arn {
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Threads = kW4Warps * 32;
+constexpr int kW4MaxWarps = 16;
 constexpr int kW4UnitK = 128;  // k of a unit
 
 struct W4Args {
@@ -64,17 +68,23 @@ struct W4Args {
   int row_blocks;   // items of a column set
   int cols;         // most columns of a set
   int split;        // CTAs of a cluster
-  int xs_offset, red_offset, part_offset, ids_offset;  // shared memory
+  int team;         // warps of a team
+  int xs_offset, sum_offset, red_offset, ids_offset;  // shared memory
   int smem_bytes;
   int *status;
 };
 
-template <int R>
-__host__ __device__ constexpr int w4_depth() {  // units of a warp's ring
-  return R == 1 ? 8 : R == 2 ? 5 : 3;
+// Units of a warp's ring: two to five in flight behind the one in use, 64 KB
+// or more an SM with the plan's warps.
+__host__ __device__ constexpr int w4_depth(int r) { return r == 1 ? 6 : 3; }
+__host__ __device__ constexpr int w4_row_bytes(int group) {
+  return group == 32 ? 112 : group == 64 ? 96 : 64;
 }
-__host__ __device__ constexpr int w4_row_bytes(int group) { return group == 32 ? 112 : 80; }
-__host__ __device__ constexpr int w4_zero_offset(int group) { return group == 32 ? 96 : 72; }
+// Scales and zero points of a row: behind its weights, or with groups of 128
+// behind the unit's.
+__host__ __device__ constexpr int w4_slot_bytes(int r, int group) {
+  return 16 * r * (w4_row_bytes(group) + (group == 128 ? 8 : 0));
+}
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -100,14 +110,38 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights I and I + 4 of a word, minus the zero point: exact in bf16.
-// `minus` holds 128 + z twice.
+// 16 + weight I and I + 4 of a word.
 template <int I>
-__device__ __forceinline__ uint32_t weight_pair(uint32_t word, uint32_t minus) {
-  const uint32_t v = ((word >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&minus));
-  return *reinterpret_cast<const uint32_t *>(&d);
+__device__ __forceinline__ uint32_t weight_pair(uint32_t word) {
+  const uint32_t v = I == 0 ? word << 3 : word >> (4 * I - 3);
+  return (v & 0x00780078u) | 0x41804180u;
+}
+
+// Words 0 .. 3 of lane t of a row (the order of the steps).
+template <int G>
+__device__ __forceinline__ void load_words(uint32_t (&w)[4], const unsigned char *row, int t) {
+  if constexpr (G == 128) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(row + t * 16);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (G == 64) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(row + t * 8);
+    const uint2 v = *reinterpret_cast<const uint2 *>(row + 32 + t * 8);
+    w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(row + i * 16 + t * 4);
+  }
+}
+// Where the eight k number k8 of a unit stand: step * 4 + lane.
+template <int G>
+__device__ __forceinline__ int step_lane(int k8) {
+  if constexpr (G == 128) return (k8 & 3) * 4 + (k8 >> 2);
+  if constexpr (G == 64) return ((k8 >> 3) * 2 + (k8 & 1)) * 4 + ((k8 >> 1) & 3);
+  return k8;
+}
+
+__device__ __forceinline__ void prefetch_line(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ float ld_cluster_f32(const float *local, uint32_t rank) {
@@ -135,42 +169,71 @@ __device__ __forceinline__ int w4_row(const W4Args &a, int block, int lr) {
   return min(block * 16 * R + lr, a.N - 1);
 }
 
-template <int R, int NT, int G, bool EXPERTS>
-__global__ void __launch_bounds__(kW4Threads) k_w4_matvec(const __grid_constant__ W4Args a) {
+// ST: AR_TYPE_* of the scales; ZEROS: whether there are zero points.
+template <int R, int NT, int G, int ST, bool ZEROS, bool EXPERTS>
+__global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(16) unsigned char w4_smem[];
-  constexpr int kDepth = w4_depth<R>();
-  constexpr int kRowBytes = w4_row_bytes(G), kZeroOffset = w4_zero_offset(G);
-  constexpr int kSlot = 16 * R * kRowBytes;
+  constexpr int kDepth = w4_depth(R), kSlot = w4_slot_bytes(R, G);
+  constexpr int kRowBytes = w4_row_bytes(G);
   constexpr int kGroups = kW4UnitK / G;  // groups of a unit
   constexpr int kRows = 16 * R;
+  // Of local row lr: its scale words at lr * kScaleStride + kScaleAt, its
+  // zero points kZeroAt behind them.
+  constexpr int kScaleAt = G == 128 ? kRows * 64 : 64;
+  constexpr int kScaleStride = G == 128 ? 8 : kRowBytes;
+  constexpr int kZeroAt = G == 128 ? 4 : G == 64 ? 8 : 32;
+  constexpr int kScaleBytes = ST == AR_TYPE_F32 ? 4 : 2;
+  // Aligned words that hold a unit's scales, or zero points, of one row.
+  constexpr int kScaleWords = ST == AR_TYPE_F32 ? kGroups : kGroups == 1 ? 1 : kGroups / 2 + 1;
+  constexpr int kZeroWords = kGroups == 1 ? 1 : 2;
 
+  const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int S = a.split;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster_id = static_cast<int>(blockIdx.x) / S, clusters = static_cast<int>(gridDim.x) / S;
   const int units = (a.units - rank + S - 1) / S;  // this CTA's units of an item
+  const int teams = warps / a.team, team = warp / a.team, member = warp % a.team;
+  const int64_t row_bytes = a.K / 2;
 
   unsigned char *ring = w4_smem + warp * (kDepth * kSlot);
   uint4 *xs = reinterpret_cast<uint4 *>(w4_smem + a.xs_offset);
+  float *xsum = reinterpret_cast<float *>(w4_smem + a.sum_offset);
   float *red = reinterpret_cast<float *>(w4_smem + a.red_offset);
-  float *part = reinterpret_cast<float *>(w4_smem + a.part_offset);
 
   // Experts: ids16[p] the expert of pair p (-1: none), sets[e] the number of
   // column sets before expert e.
   int16_t *ids16 = reinterpret_cast<int16_t *>(w4_smem + a.ids_offset);
-  __shared__ int sets[AR_MAX_EXPERTS + 1];
+  __shared__ int sets[EXPERTS ? AR_MAX_EXPERTS + 1 : 1];
   __shared__ int col_pair[8 * NT];
   __shared__ int col_count;
+  __shared__ uint4 zero16;
 
+  int nsets = (a.pairs + a.cols - 1) / a.cols;
+  if constexpr (!EXPERTS) {
+    // The first units' lines on their way to L2 while the previous grid
+    // drains: nothing enters this SM before the wait.
+    const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
+    const int64_t item = total * cluster_id / clusters + team;
+    if (item < total * (cluster_id + 1) / clusters && (t & 1) == 0) {
+      const int block = static_cast<int>(item % a.row_blocks);
+      for (int d = 0, lu = member; d < kDepth - 1 && lu < units; ++d, lu += a.team) {
+        const int64_t piece = static_cast<int64_t>(lu * S + rank) * 64 + t * 16;
+#pragma unroll
+        for (int i = 0; i < 2 * R; ++i)
+          if (piece < row_bytes)
+            prefetch_line(a.q + w4_row<R>(a, block, g + 8 * i) * row_bytes + piece);
+      }
+    }
+  }
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  int nsets = (a.pairs + a.cols - 1) / a.cols;
   if constexpr (EXPERTS) {
-    for (int e = tid; e <= AR_MAX_EXPERTS; e += kW4Threads) sets[e] = 0;
+    for (int e = tid; e <= AR_MAX_EXPERTS; e += threads) sets[e] = 0;
     __syncthreads();
-    for (int p = tid; p < a.pairs; p += kW4Threads) {
+    for (int p = tid; p < a.pairs; p += threads) {
       const int e = __ldg(a.ids + p);
       const bool ok = e >= 0 && e < a.E;
       ids16[p] = static_cast<int16_t>(ok ? e : -1);
@@ -200,7 +263,7 @@ __global__ void __launch_bounds__(kW4Threads) k_w4_matvec(const __grid_constant_
     // Pairs without an expert here: zero rows, spread over the grid.
     for (int p = blockIdx.x; p < a.pairs; p += gridDim.x)
       if (ids16[p] < 0)
-        for (int n = tid; n < a.width; n += kW4Threads)
+        for (int n = tid; n < a.width; n += threads)
           a.out[static_cast<int64_t>(p) * a.width + n] = __float2bfloat16_rn(0.f);
   }
   const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
@@ -219,277 +282,324 @@ __global__ void __launch_bounds__(kW4Threads) k_w4_matvec(const __grid_constant_
     return lo;
   };
 
-  // Issue side of the ring: the next unit to fetch.
-  int f_item = item0, f_unit = warp, f_slot = 0;
-  int f_set = -1, f_block = 0;
-  int64_t f_expert_row = 0;  // first row of W of the item's expert
-  const int64_t row_bytes = a.K / 2;
+  // The fetching side of the ring.  f_item: the team's item, f_end: the end
+  // of its column set's part of the range.
+  int f_item = item0 + team, f_end = item0, f_unit = member, f_slot = 0;
+  const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the expert's first row
+  uint32_t f_off[2 * R];         // the rows' distances, in 16 bytes
+  const uint8_t *f_s = nullptr, *f_z = nullptr;  // scales and zero points of row `lane`
+  auto next_item = [&]() {        // from f_item on, the team's first item that exists
+    while (f_item >= f_end && f_end < item1) {
+      const int set = f_end / a.row_blocks;
+      f_item = f_end + team;
+      f_end = min(item1, (set + 1) * a.row_blocks);
+    }
+    if (f_item >= f_end) return;
+    const int set = f_item / a.row_blocks, block = f_item - set * a.row_blocks;
+    const int64_t first = static_cast<int64_t>(expert_of(set)) * a.N;
+    f_q = a.q + first * row_bytes + t * 16;
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i)
+      f_off[i] = static_cast<uint32_t>(w4_row<R>(a, block, g + 8 * i)) *
+                 static_cast<uint32_t>(row_bytes >> 4);
+    const int64_t el = (first + w4_row<R>(a, block, lane & (kRows - 1))) * a.ng;
+    f_s = a.scales + el * kScaleBytes;
+    if constexpr (ZEROS) f_z = a.zeros + el;
+  };
+  next_item();
   auto fetch = [&]() {
-    if (f_item < item1 && f_unit < units) {
-      const int set = f_item / a.row_blocks;
-      if (set != f_set) {
-        f_set = set;
-        f_expert_row = static_cast<int64_t>(expert_of(set)) * a.N;
-      }
-      f_block = f_item - set * a.row_blocks;
+    while (f_item < f_end && f_unit >= units) {
+      // The team's warps take up the next item where this one left them.
+      f_unit -= units;
+      f_item += teams;
+      next_item();
+    }
+    if (f_item < f_end) {
       const int u = f_unit * S + rank;
       const uint32_t slot = smem_addr(ring + f_slot * kSlot);
-      const int piece = u * 64 + t * 16;  // byte of the row
-      const uint32_t bytes = piece < row_bytes ? 16u : 0u;
+      const bool here = u * 64 + t * 16 < static_cast<int>(row_bytes);
+      const uint8_t *src = f_q + (here ? u * 64 : 0);
+      const uint32_t bytes = here ? 16u : 0u;
 #pragma unroll
-      for (int i = 0; i < 2 * R; ++i) {
-        const int lr = g + 8 * i;
-        const int64_t row = f_expert_row + w4_row<R>(a, f_block, lr);
-        cp_async_16(slot + lr * kRowBytes + t * 16, a.q + row * row_bytes + (bytes ? piece : 0),
-                    bytes);
-      }
-      // The aligned words around the unit's scales and zero points.
-      const int size_log2 = a.scale_type == AR_TYPE_F32 ? 2 : 1;
+      for (int i = 0; i < 2 * R; ++i)
+        cp_async_16(slot + (g + 8 * i) * kRowBytes + t * 16,
+                    src + static_cast<uint64_t>(f_off[i]) * 16, bytes);
+      // The aligned words around the unit's scales and zero points, cut off
+      // at the end of their arrays.
+      if (lane < kRows) {
+        const uint32_t to = slot + kScaleAt + lane * kScaleStride;
+        auto words = [&](uint32_t dst, const uint8_t *p, const uint8_t *end, int n) {
+          const uint8_t *w = p - (reinterpret_cast<uintptr_t>(p) & 3);
 #pragma unroll
-      for (int i = 0; i < (kRows + 31) / 32; ++i) {
-        const int lr = lane + 32 * i;
-        if (lr < kRows) {
-          const int64_t row = f_expert_row + w4_row<R>(a, f_block, lr);
-          const int64_t el = row * a.ng + u * kGroups;
-          const int64_t sb = (el << size_log2) & ~int64_t{3};
-          const int words = a.scale_type == AR_TYPE_F32 ? kGroups : kGroups == 1 ? 1 : kGroups / 2 + 1;
-          for (int w = 0; w < words; ++w) {
-            const int64_t left = a.scale_bytes - (sb + 4 * w);
-            const uint32_t n = left >= 4 ? 4u : left > 0 ? static_cast<uint32_t>(left) : 0u;
-            cp_async_4(slot + lr * kRowBytes + 64 + 4 * w, a.scales + (n ? sb + 4 * w : 0), n);
+          for (int i = 0; i < n; ++i) {
+            const int64_t left = end - (w + 4 * i);
+            if (left > 0) cp_async_4(dst + 4 * i, w + 4 * i, left < 4 ? static_cast<uint32_t>(left) : 4u);
           }
-          if (a.zeros != nullptr) {
-            const int64_t zb = el & ~int64_t{3};
-#pragma unroll
-            for (int w = 0; w < (kGroups == 1 ? 1 : 2); ++w) {
-              const int64_t left = a.zero_bytes - (zb + 4 * w);
-              const uint32_t n = left >= 4 ? 4u : left > 0 ? static_cast<uint32_t>(left) : 0u;
-              cp_async_4(slot + lr * kRowBytes + kZeroOffset + 4 * w, a.zeros + (n ? zb + 4 * w : 0),
-                         n);
-            }
-          }
-        }
+        };
+        words(to, f_s + u * (kGroups * kScaleBytes), a.scales + a.scale_bytes, kScaleWords);
+        if constexpr (ZEROS) words(to + kZeroAt, f_z + u * kGroups, a.zeros + a.zero_bytes, kZeroWords);
       }
       f_slot = f_slot + 1 == kDepth ? 0 : f_slot + 1;
-      f_unit += kW4Warps;
-      if (f_unit >= units) {
-        f_unit = warp;
-        ++f_item;
-      }
+      f_unit += a.team;
     }
     cp_async_commit();  // an empty group at the end keeps the count
   };
 #pragma unroll 1
   for (int i = 0; i < kDepth - 1; ++i) fetch();
 
-  int slot_at = 0, staged = -1, ncols = 0, parity = 0;
+  const bool act = a.act == AR_ACT_SILU_MUL;
+  const int outs = act ? 8 * R : kRows;  // outputs of an item's column
+  int c_unit = member, slot_at = 0, parity = 0;
 #pragma unroll 1
-  for (int item = item0; item < item1; ++item) {
-    const int set = item / a.row_blocks, block = item - set * a.row_blocks;
+  for (int seg = item0; seg < item1;) {
+    // The part of the range that has one column set.
+    const int set = seg / a.row_blocks;
+    const int seg_end = min(item1, (set + 1) * a.row_blocks);
     const int expert = expert_of(set);
-    if (set != staged) {
-      // The set's columns, in the order of the pairs, then their x.
-      staged = set;
-      __syncthreads();
-      if constexpr (EXPERTS) {
-        if (warp == 0) {
-          const int skip = (set - sets[expert]) * a.cols;
-          int seen = 0;
-          for (int p0 = 0; p0 < a.pairs && seen < skip + a.cols; p0 += 32) {
-            const bool is = p0 + lane < a.pairs && ids16[p0 + lane] == expert;
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
-            const int at = seen + __popc(who & ((1u << lane) - 1u)) - skip;
-            if (is && at >= 0 && at < a.cols) col_pair[at] = p0 + lane;
-            seen += __popc(who);
-          }
-          if (lane == 0) col_count = min(seen - skip, a.cols);
+    __syncthreads();  // nobody uses the last set's x any more
+    if (tid == 0) zero16 = make_uint4(0, 0, 0, 0);
+    if constexpr (EXPERTS) {
+      if (warp == 0) {  // the set's columns, in the order of the pairs
+        const int skip = (set - sets[expert]) * a.cols;
+        int seen = 0;
+        for (int p0 = 0; p0 < a.pairs && seen < skip + a.cols; p0 += 32) {
+          const bool is = p0 + lane < a.pairs && ids16[p0 + lane] == expert;
+          const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
+          const int at = seen + __popc(who & ((1u << lane) - 1u)) - skip;
+          if (is && at >= 0 && at < a.cols) col_pair[at] = p0 + lane;
+          seen += __popc(who);
         }
-      } else {
-        if (tid < min(a.cols, a.pairs - set * a.cols)) col_pair[tid] = set * a.cols + tid;
-        if (tid == 0) col_count = min(a.cols, a.pairs - set * a.cols);
+        if (lane == 0) col_count = min(seen - skip, a.cols);
       }
-      __syncthreads();
-      ncols = col_count;
-      const int pieces = units * 16;
-      for (int i = tid; i < pieces * ncols; i += kW4Threads) {
-        const int col = i / pieces, j = i - col * pieces;  // j: (unit, 32, eight)
-        const int k8 = ((j >> 4) * S + rank) * 16 + (j & 15);  // eight of the row
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (k8 * 8 < a.K) {
-          const int64_t row = col_pair[col] / a.k;
-          const uint4 w = __ldg(a.x + row * (a.K / 8) + k8);
-          v = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
+    } else {
+      const int n = min(a.cols, a.pairs - set * a.cols);
+      if (tid < n) col_pair[tid] = set * a.cols + tid;
+      if (tid == 0) col_count = n;
+    }
+    __syncthreads();
+    const int ncols = col_count;
+    {
+      const int pieces = units * 16;  // eights of a column
+      for (int i0 = 0; i0 < pieces * ncols; i0 += threads) {
+        const int i = i0 + tid, col = i / pieces, j = i - col * pieces;
+        const int lu = j >> 4, k8 = j & 15, at = (lu * S + rank) * 16 + k8;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (col < ncols && at * 8 < a.K)
+          w = __ldg(a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + at);
+        float f[8];
+        unpack8(w, f);
+        float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+#pragma unroll
+        for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (col < ncols) {
+          const int to = step_lane<G>(k8);
+          xs[((lu * 4 + (to >> 2)) * a.cols + col) * 4 + (to & 3)] =
+              make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
                          __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+          if (k8 % (G / 8) == 0) xsum[(lu * kGroups + k8 / (G / 8)) * (8 * NT) + col] = sum;
         }
-        xs[((j >> 2) * a.cols + col) * 4 + (j & 3)] = v;
       }
-      __syncthreads();
     }
+    __syncthreads();
 
-    float acc[R][NT][4];
-    int el_low[R][2];  // low bits of the rows' first group number
+    // This lane's eights of x: column g of each tile, or zeros.
+    const uint4 *xp[NT];
+    int xstep[NT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        el_low[r][h] = static_cast<int>(
-            ((static_cast<int64_t>(expert) * a.N + w4_row<R>(a, block, r * 16 + h * 8 + g)) * a.ng) & 3);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][n][c] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      const bool in = n * 8 + g < ncols;
+      xp[n] = in ? xs + (n * 8 + g) * 4 + t : &zero16;
+      xstep[n] = in ? a.cols * 4 : 0;
     }
+    const int rounds = (seg_end - seg + teams - 1) / teams;
 #pragma unroll 1
-    for (int lu = warp; lu < units; lu += kW4Warps) {
-      cp_async_wait<kDepth - 2>();
-      __syncwarp();  // every lane's copies are here, and the slot before is free
-      fetch();
-      const unsigned char *slot = ring + slot_at * kSlot;
-      slot_at = slot_at + 1 == kDepth ? 0 : slot_at + 1;
-      const int u0 = (lu * S + rank) * kGroups;
-      float d[R][NT][4];
-      float s[R][2];
-      uint32_t minus[R][2];
+    for (int round = 0; round < rounds; ++round) {
+      const int item = seg + round * teams + team;
+      const bool has = item < seg_end;
+      const int block = item - set * a.row_blocks;
+      float acc[R][NT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        constexpr int kPer = G / 32;  // 32s of a group
-        const int gi = i / kPer;
-        if (i % kPer == 0) {
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const unsigned char *row = slot + (r * 16 + h * 8 + g) * kRowBytes;
-              const int low = (el_low[r][h] + u0) & 3;
-              if (a.scale_type == AR_TYPE_F32) {
-                s[r][h] = *reinterpret_cast<const float *>(row + 64 + gi * 4);
-              } else {
-                const uint16_t b =
-                    *reinterpret_cast<const uint16_t *>(row + 64 + ((low & 1) + gi) * 2);
-                s[r][h] = a.scale_type == AR_TYPE_BF16
-                              ? __uint_as_float(static_cast<uint32_t>(b) << 16)
-                              : __half2float(__ushort_as_half(b));
-              }
-              if (u0 + gi >= a.ng) s[r][h] = 0.f;  // behind the row: another row's scale
-              const uint32_t z = a.zeros != nullptr ? row[kZeroOffset + low + gi] & 15u : 8u;
-              minus[r][h] = 0x43004300u | z | (z << 16);
-            }
+          for (int c = 0; c < 4; ++c) acc[r][n][c] = 0.f;
+      if (has) {
+        int el_low[R][2];  // low bits of the rows' first group numbers
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) d[r][n][c] = 0.f;
-          }
-        }
-        uint4 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          b[n] = make_uint4(0, 0, 0, 0);
-          if (n * 8 + g < ncols) b[n] = xs[((lu * 4 + i) * a.cols + n * 8 + g) * 4 + t];
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const unsigned char *at = slot + (r * 16 + g) * kRowBytes + i * 16 + t * 4;
-          const uint32_t w0 = *reinterpret_cast<const uint32_t *>(at);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t *>(at + 8 * kRowBytes);
-          const uint32_t p0 = weight_pair<0>(w0, minus[r][0]), p1 = weight_pair<0>(w1, minus[r][1]);
-          const uint32_t p2 = weight_pair<1>(w0, minus[r][0]), p3 = weight_pair<1>(w1, minus[r][1]);
-          const uint32_t p4 = weight_pair<2>(w0, minus[r][0]), p5 = weight_pair<2>(w1, minus[r][1]);
-          const uint32_t p6 = weight_pair<3>(w0, minus[r][0]), p7 = weight_pair<3>(w1, minus[r][1]);
+          for (int h = 0; h < 2; ++h)
+            el_low[r][h] =
+                ((expert * a.N + w4_row<R>(a, block, r * 16 + h * 8 + g)) & 3) * (a.ng & 3);
+#pragma unroll 1
+        for (; c_unit < units; c_unit += a.team) {
+          cp_async_wait<kDepth - 2>();
+          __syncwarp();  // every lane's copies are here, and the slot before is free
+          fetch();
+          const unsigned char *slot = ring + slot_at * kSlot;
+          slot_at = slot_at + 1 == kDepth ? 0 : slot_at + 1;
+          uint4 b[4][NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_bf16(d[r][n], p0, p1, p2, p3, b[n].x, b[n].y);
-            mma_bf16(d[r][n], p4, p5, p6, p7, b[n].z, b[n].w);
+            const uint4 *p = xp[n] + c_unit * 4 * xstep[n];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i][n] = p[i * xstep[n]];
+          }
+          const int u0 = (c_unit * S + rank) * kGroups;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const unsigned char *row = slot + (r * 16 + g) * kRowBytes;
+            uint32_t w0[4], w1[4];
+            load_words<G>(w0, row, t);
+            load_words<G>(w1, row + 8 * kRowBytes, t);
+            const unsigned char *sc = slot + kScaleAt + (r * 16 + g) * kScaleStride;
+#pragma unroll
+            for (int gi = 0; gi < kGroups; ++gi) {
+              // Scale and offset of the two rows' group.
+              float s[2], off[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const unsigned char *p = sc + h * 8 * kScaleStride;
+                const int low = el_low[r][h] + u0;
+                if constexpr (ST == AR_TYPE_F32) {
+                  s[h] = *reinterpret_cast<const float *>(p + gi * 4);
+                } else {
+                  const uint16_t v = *reinterpret_cast<const uint16_t *>(p + ((low & 1) + gi) * 2);
+                  s[h] = ST == AR_TYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16)
+                                            : __half2float(__ushort_as_half(v));
+                }
+                // Behind the row's end stands another row's scale.
+                if (kGroups > 1 && u0 + gi >= a.ng) s[h] = 0.f;
+                off[h] = 24.f;
+                if constexpr (ZEROS)
+                  off[h] = 16.f + static_cast<float>(p[kZeroAt + (low & 3) + gi] & 15u);
+              }
+              float d[NT][4];
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) d[n][c] = 0.f;
+              constexpr int kSteps = 4 / kGroups;
+#pragma unroll
+              for (int i = gi * kSteps; i < (gi + 1) * kSteps; ++i) {
+                const uint32_t p0 = weight_pair<0>(w0[i]), p1 = weight_pair<0>(w1[i]);
+                const uint32_t p2 = weight_pair<1>(w0[i]), p3 = weight_pair<1>(w1[i]);
+                const uint32_t p4 = weight_pair<2>(w0[i]), p5 = weight_pair<2>(w1[i]);
+                const uint32_t p6 = weight_pair<3>(w0[i]), p7 = weight_pair<3>(w1[i]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  mma_bf16(d[n], p0, p1, p2, p3, b[i][n].x, b[i][n].y);
+                  mma_bf16(d[n], p4, p5, p6, p7, b[i][n].z, b[i][n].w);
+                }
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const float2 xg = *reinterpret_cast<const float2 *>(
+                    xsum + (c_unit * kGroups + gi) * (8 * NT) + n * 8 + 2 * t);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  acc[r][n][c] = fmaf(s[c >> 1], fmaf(-off[c >> 1], c & 1 ? xg.y : xg.x, d[n][c]),
+                                      acc[r][n][c]);
+              }
+            }
           }
         }
-        if (i % kPer == kPer - 1) {
+        c_unit -= units;
+      }
+
+      // Where the item's column and row end up, and what they hold.
+      auto store = [&](int col, int o, float v) {
+        const int n = block * outs + o;
+        if (n < a.width)
+          a.out[static_cast<int64_t>(col_pair[col]) * a.width + n] = __float2bfloat16_rn(v);
+      };
+      if (a.team == 1 && S == 1) {  // the warp has the whole sums
+        if (has) {
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) acc[r][n][c] = fmaf(s[r][c >> 1], d[r][n][c], acc[r][n][c]);
+              for (int c = 0; c < 4; ++c) {
+                const int col = n * 8 + 2 * t + (c & 1);
+                if (col >= ncols) continue;
+                if (!act) store(col, r * 16 + (c >> 1) * 8 + g, acc[r][n][c]);
+                else if (c < 2) store(col, r * 8 + g, gated(acc[r][n][c], acc[r][n][c + 2]));
+              }
         }
+        continue;
       }
-    }
-
-    // The warps' sums, in order: red[warp][column][row].
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = n * 8 + 2 * t + (c & 1), row = r * 16 + (c >> 1) * 8 + g;
-          if (col < ncols) red[(warp * a.cols + col) * kRows + row] = acc[r][n][c];
-        }
-    __syncthreads();
-    const int warp_stride = a.cols * kRows;
-    auto cta_sum = [&](int col, int row) -> float {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW4Warps; ++w) v += red[w * warp_stride + col * kRows + row];
-      return v;
-    };
-    float *mine = part + parity * warp_stride;
-    if (S > 1) {
-      for (int i = tid; i < ncols * kRows; i += kW4Threads) mine[i] = cta_sum(i / kRows, i % kRows);
-      __syncwarp();
-      // Double-buffered: a buffer is written again two items on, after a
-      // barrier that every CTA reaches only behind its reads of it.
-      cluster_arrive_release();
-      cluster_wait_acquire();
+      // The warps' sums: red[parity][warp][column][row].  A buffer is written
+      // again two items on, behind a barrier that every reader has passed.
+      const int stride = a.cols * kRows;
+      float *buf = red + (parity * warps + team * a.team) * stride;
       parity ^= 1;
-    }
-    auto item_sum = [&](int col, int row) -> float {
-      if (S == 1) return cta_sum(col, row);
-      float v = 0.f;
-      for (int c = 0; c < S; ++c) v += ld_cluster_f32(mine + col * kRows + row, c);
-      return v;
-    };
-    const bool act = a.act == AR_ACT_SILU_MUL;
-    const int outs = act ? 8 * R : kRows;  // outputs of an item's column
-    for (int i = tid * S + rank; i < ncols * outs; i += kW4Threads * S) {
-      const int col = i / outs, o = i % outs;
-      const int n = block * outs + o;
-      if (n >= a.width) continue;
-      float v;
-      if (act) {
-        const int row = (o >> 3) * 16 + (o & 7);
-        v = gated(item_sum(col, row), item_sum(col, row + 8));
-      } else {
-        v = item_sum(col, o);
+      if (has) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int col = n * 8 + 2 * t + (c & 1), row = r * 16 + (c >> 1) * 8 + g;
+              if (col < ncols) buf[member * stride + col * kRows + row] = acc[r][n][c];
+            }
       }
-      a.out[static_cast<int64_t>(col_pair[col]) * a.width + n] = __float2bfloat16_rn(v);
+      if (S > 1) {
+        __syncwarp();
+        cluster_arrive_release();
+        cluster_wait_acquire();
+      } else if (has) {
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(a.team * 32) : "memory");
+      }
+      if (has) {
+        auto sum_of = [&](int col, int row) -> float {
+          float v = 0.f;
+          const float *p = buf + col * kRows + row;
+          if (S == 1) {
+            for (int w = 0; w < a.team; ++w) v += p[w * stride];
+          } else {
+            for (int c = 0; c < S; ++c)
+              for (int w = 0; w < a.team; ++w) v += ld_cluster_f32(p + w * stride, c);
+          }
+          return v;
+        };
+        for (int i = (member * 32 + lane) * S + rank; i < ncols * outs; i += a.team * 32 * S) {
+          const int col = i / outs, o = i - col * outs;
+          if (act) {
+            const int row = (o >> 3) * 16 + (o & 7);
+            store(col, o, gated(sum_of(col, row), sum_of(col, row + 8)));
+          } else {
+            store(col, o, sum_of(col, o));
+          }
+        }
+      }
     }
-    __syncthreads();  // red, and col_pair before the next set
+    seg = seg_end;
   }
   cp_async_wait<0>();
   if (S > 1) {  // no CTA leaves while another reads its sums
+    __syncwarp();
     cluster_arrive_release();
     cluster_wait_acquire();
   }
 }
 
 using W4Kernel = void (*)(W4Args);
-// [row tiles 1, 2, 4][column tiles 1, 2][group 32, 64, 128]
-W4Kernel w4_dense_kernel(int r, int nt, int group);
-W4Kernel w4_experts_kernel(int r, int nt, int group);
-
-template <bool EXPERTS, int R, int NT>
+template <int ST, bool ZEROS, bool EXPERTS, int R, int NT>
 inline W4Kernel w4_pick_group(int group) {
-  return group == 32 ? &k_w4_matvec<R, NT, 32, EXPERTS>
-         : group == 64 ? &k_w4_matvec<R, NT, 64, EXPERTS>
-                       : &k_w4_matvec<R, NT, 128, EXPERTS>;
+  return group == 32 ? &k_w4_matvec<R, NT, 32, ST, ZEROS, EXPERTS>
+         : group == 64 ? &k_w4_matvec<R, NT, 64, ST, ZEROS, EXPERTS>
+                       : &k_w4_matvec<R, NT, 128, ST, ZEROS, EXPERTS>;
 }
-template <bool EXPERTS>
-inline W4Kernel w4_pick(int r, int nt, int group) {
+template <int ST, bool ZEROS, bool EXPERTS>
+inline W4Kernel w4_pick_tile(int r, int nt, int group) {
   if (nt == 1)
-    return r == 1 ? w4_pick_group<EXPERTS, 1, 1>(group)
-           : r == 2 ? w4_pick_group<EXPERTS, 2, 1>(group)
-                    : w4_pick_group<EXPERTS, 4, 1>(group);
-  return r == 1 ? w4_pick_group<EXPERTS, 1, 2>(group)
-         : r == 2 ? w4_pick_group<EXPERTS, 2, 2>(group)
-                  : w4_pick_group<EXPERTS, 4, 2>(group);
+    return r == 1 ? w4_pick_group<ST, ZEROS, EXPERTS, 1, 1>(group)
+                  : w4_pick_group<ST, ZEROS, EXPERTS, 2, 1>(group);
+  return r == 1 ? w4_pick_group<ST, ZEROS, EXPERTS, 1, 2>(group)
+                : w4_pick_group<ST, ZEROS, EXPERTS, 2, 2>(group);
 }
 
 }  // namespace arn

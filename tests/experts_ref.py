@@ -62,23 +62,26 @@ def unpack(q, scales, zeros):
     return (w - z) * scales.double().repeat_interleave(group, -1)
 
 
-def product(x, w):
-    """x [r, K] times w [N, K]: (sums, sums of magnitudes)."""
+def product(x, q, scales, zeros):
+    """x [r, K] times 4-bit weights [N, K/2]: (sums, error of an fp32 product).
+
+    Per group, 16 + q is multiplied by x and summed, and 16 + z times the sum
+    of x comes off: both are at most 31 sum |x|.  A matrix instruction adds
+    16 products to a running sum (at most 2^-23 of the magnitudes so far,
+    truncation included), G/16 of them; the sum of x is a tree of at most 8
+    roundings; the subtraction and the scale round once each.  The groups'
+    sums of magnitudes at most (31 + 31) |s| sum |x| then pass K/128 adds at
+    most, and up to 128 joining warps and CTAs."""
+    K = x.shape[1]
+    group = K // scales.shape[-1]
     x = x.double()
-    return x @ w.T, x.abs() @ w.abs().T
+    mag = 62 * (x.abs() @ scales.double().abs().repeat_interleave(group, -1).T)
+    roundings = 2 * group / 16 + 8 + 2 + K / 128 + 128
+    return x @ unpack(q, scales, zeros).T, roundings * F32 * mag
 
 
-def product_bound(magnitude, K):
-    """fp32 error of a product: every one of the K / 16 matrix instructions
-    adds 16 products to a running sum (at most 2^-23 of the magnitudes so
-    far, truncation included), a group's scale rounds once, and at most
-    K / 128 + 16 adds join the groups, warps and CTAs."""
-    return (K / 16 + K / 32 + K / 128 + 16) * 2 * F32 * magnitude
-
-
-def act(y, mag, K, kind):
+def act(y, err, kind):
     """(result, error bound before the last rounding) of a product's epilogue."""
-    err = product_bound(mag, K)
     if kind == "none":
         return y, err
     h = y.shape[-1] // 2

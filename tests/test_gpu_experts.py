@@ -219,7 +219,7 @@ def test_w4_matvec(m, K, N, group, kind, zeros, act):
     arn.ar_w4_matvec(x, q, s, zeros=z, act=act, out=out)
     torch.cuda.synchronize()
     assert intact()
-    y, err = ref.act(*ref.product(x, ref.unpack(q, s, z)), K, act)
+    y, err = ref.act(*ref.product(x, q, s, z), act)
     ref.close(out, y, err)
 
 
@@ -254,8 +254,8 @@ def expert_rows(x, ids, q, s, z, act):
     for ex in range(q.shape[0]):
         at = (flat == ex).nonzero().flatten()
         if len(at):
-            w = ref.unpack(q[ex], s[ex], None if z is None else z[ex])
-            y[at], e[at] = ref.act(*ref.product(rows[at], w), K, act)
+            y[at], e[at] = ref.act(*ref.product(rows[at], q[ex], s[ex],
+                                                None if z is None else z[ex]), act)
     return y.view(m, k, -1), e.view(m, k, -1)
 
 
@@ -489,9 +489,8 @@ def test_a_given_stream_owns_its_outputs():
         assert torch.equal(w, want) and torch.equal(ids, ids0) and bool(o.isfinite().all())
 
 
-def test_results_do_not_depend_on_the_company():
-    """A row's product is the same bits alone, in a batch, and with other
-    tokens at its expert."""
+def test_results_repeat_bit_for_bit():
+    """No atomics in any sum: the same call gives the same bits."""
     g = gen(51)
     x = normal(g, 16, 1024)
     q, s, z = weights4(g, (8, 96), 1024, 128, "bf16", True)
