@@ -69,8 +69,6 @@ static int64_t w4_layout(const W4Plan &p, int group, int units, int pairs, bool 
   int64_t at = int64_t{p.warps} * w4_depth(p.r) * w4_slot_bytes(p.r, group);
   a->xs_offset = static_cast<int>(at);
   at += slice * 256 * p.cols;
-  a->sum_offset = static_cast<int>(at);
-  at += slice * (kW4UnitK / group) * 8 * p.nt * 4;
   a->red_offset = static_cast<int>(at);
   if (p.team > 1 || p.split > 1) at += int64_t{2} * p.warps * p.cols * 16 * p.r * 4;
   a->ids_offset = static_cast<int>(at);
@@ -142,8 +140,7 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.scales = static_cast<const uint8_t *>(scales);
   a.zeros = static_cast<const uint8_t *>(zeros);
   a.out = static_cast<__nv_bfloat16 *>(out);
-  a.scale_bytes = E * N * ng * size;
-  a.zero_bytes = E * N * ng;
+  a.scale_count = E * N * ng;
   a.pairs = static_cast<int>(pairs);
   a.k = x_per_pair ? 1 : k;
   a.E = E;

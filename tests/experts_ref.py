@@ -65,19 +65,19 @@ def unpack(q, scales, zeros):
 def product(x, q, scales, zeros):
     """x [r, K] times 4-bit weights [N, K/2]: (sums, error of an fp32 product).
 
-    Per group, 16 + q is multiplied by x and summed, and 16 + z times the sum
-    of x comes off: both are at most 31 sum |x|.  A matrix instruction adds
-    16 products to a running sum (at most 2^-23 of the magnitudes so far,
-    truncation included), G/16 of them; the sum of x is a tree of at most 8
-    roundings; the subtraction and the scale round once each.  The groups'
-    sums of magnitudes at most (31 + 31) |s| sum |x| then pass K/128 adds at
-    most, and up to 128 joining warps and CTAs."""
+    A matrix instruction adds 16 products to a running sum (at most 2^-23 of
+    the magnitudes so far, truncation included), G/16 of them a group; the
+    scale rounds once; the groups' sums pass K/128 adds at most, and up to
+    128 joining warps and CTAs.  The magnitudes: sum |q - z| |s| |x|.  x
+    itself is exact down to 2^-30 of its row's largest and off by at most
+    2^-39 of that below, for weights of at most 15 |s|."""
     K = x.shape[1]
     group = K // scales.shape[-1]
+    w = unpack(q, scales, zeros)
     x = x.double()
-    mag = 62 * (x.abs() @ scales.double().abs().repeat_interleave(group, -1).T)
-    roundings = 2 * group / 16 + 8 + 2 + K / 128 + 128
-    return x @ unpack(q, scales, zeros).T, roundings * F32 * mag
+    roundings = 2 * group / 16 + 1 + K / 128 + 128
+    tiny = 2.0 ** -39 * 15 * x.abs().amax(1, keepdim=True) * group * scales.double().abs().sum(1)
+    return x @ w.T, roundings * F32 * (x.abs() @ w.abs().T) + tiny
 
 
 def act(y, err, kind):

@@ -277,6 +277,21 @@ def test_w4_matvec_experts(m, E, k, K, N, group, kind, zeros, act, per_pair, mis
     assert not bool(out[gone].any())
 
 
+@pytest.mark.parametrize("level", [2.0 ** -133, 2.0 ** -126, 1e-30, 1.0, 1e30])
+def test_w4_matvec_holds_over_the_range_of_x(level):
+    """Rows from bf16's smallest to its largest numbers, and rows whose values
+    spread over sixty powers of two (scales bring the results back)."""
+    g = gen(13)
+    x = torch.randint(-8, 9, (6, 512), generator=g, device=DEV).double() * level
+    x[1] *= torch.exp2(-torch.randint(0, 60, (512,), generator=g, device=DEV).double())
+    x[2, 100] *= 2.0 ** 6
+    x[3] = 0
+    x = x.bfloat16()
+    q, s, z = weights4(g, (64,), 512, 64, "f32", True)
+    s = (s.double() / max(level, 2.0 ** -100)).float() if level < 1 else s
+    ref.close(arn.ar_w4_matvec(x, q, s, zeros=z), *ref.product(x, q, s, z))
+
+
 def test_w4_nan_and_infinite_rows_stay_their_own():
     """A NaN or an infinity in one row of x, or one scale, reaches no other
     row or output; the group behind a row's end takes no part."""
