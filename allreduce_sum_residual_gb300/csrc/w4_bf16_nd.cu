@@ -5,7 +5,7 @@
 namespace arn {
 
 W4Kernel w4_kernel_bf16_nd(int r, int nt, int group) {
-  return w4_pick_tile<AR_TYPE_BF16, false, false>(r, nt, group);
+  return w4_pick<AR_TYPE_BF16, false, false>(r, nt, group);
 }
 
 }  // namespace arn

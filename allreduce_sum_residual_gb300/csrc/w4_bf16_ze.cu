@@ -5,7 +5,7 @@
 namespace arn {
 
 W4Kernel w4_kernel_bf16_ze(int r, int nt, int group) {
-  return w4_pick_tile<AR_TYPE_BF16, true, true>(r, nt, group);
+  return w4_pick<AR_TYPE_BF16, true, true>(r, nt, group);
 }
 
 }  // namespace arn

@@ -5,7 +5,7 @@
 namespace arn {
 
 W4Kernel w4_kernel_f32_ne(int r, int nt, int group) {
-  return w4_pick_tile<AR_TYPE_F32, false, true>(r, nt, group);
+  return w4_pick<AR_TYPE_F32, false, true>(r, nt, group);
 }
 
 }  // namespace arn

@@ -46,6 +46,7 @@ static int allow_shared_memory(int bytes) {
   for (int type = AR_TYPE_F32; type <= AR_TYPE_F16; ++type)
     for (int i = 0; i < 16; ++i)
       for (int group = 32; group <= 128; group *= 2) {
+        if (group == 32 && (i & 4)) continue;  // one row tile
         const W4Kernel kern = w4_kernel(type, i & 1, i & 2, i & 4 ? 2 : 1, i & 8 ? 2 : 1, group);
         if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -59,22 +60,41 @@ static int allow_shared_memory(int bytes) {
 }
 
 struct W4Plan {
-  int r, nt, warps, team, split, cols, ctas_per_sm;
+  int r, nt, warps, team, phase_units, cols, x_cols;
   int64_t sets;  // most column sets
 };
 
-// Lays out shared memory for a plan; its bytes.
-static int64_t w4_layout(const W4Plan &p, int group, int units, int pairs, bool experts, W4Args *a) {
-  const int64_t slice = (units + p.split - 1) / p.split;  // a CTA's units of an item
-  int64_t at = int64_t{p.warps} * w4_depth(p.r) * w4_slot_bytes(p.r, group);
+// Lays out shared memory for a plan, with as many columns of x as fit into
+// `most` (and no more than sets could fill); false if not even one set does.
+static bool w4_layout(W4Plan *p, int group, int64_t most, bool experts, W4Args *a) {
+  const bool phased = p->phase_units < a->units;
+  const int64_t column = int64_t{p->phase_units} * 256;
+  const int64_t tile = int64_t{p->cols} * 16 * p->r * 4;
+  const int64_t ring = int64_t{p->warps} * w4_depth(p->r) * w4_slot_bytes(p->r, group);
+  const int64_t red = p->team > 1 ? int64_t{2} * p->warps * tile : 0;
+  const int teams = p->warps / p->team;
+  // Sums between phases: as many items a team as 32 KB hold.
+  a->phase_rounds = static_cast<int>(32768 / (teams * tile));
+  if (a->phase_rounds < 1) a->phase_rounds = 1;
+  const int64_t acc = phased ? a->phase_rounds * teams * tile : 0;
+  const int64_t ids = experts ? (int64_t{2} * a->pairs + 15) / 16 * 16 : 0;
+  int64_t x_cols = (most - ring - red - acc - ids) / column;
+  if (x_cols < p->cols) return false;
+  if (phased) x_cols = p->cols;  // a phase holds one set
+  if (x_cols > kW4MaxXCols) x_cols = kW4MaxXCols;
+  if (x_cols > a->pairs) x_cols = a->pairs;
+  p->x_cols = static_cast<int>(x_cols);
+  int64_t at = ring;
   a->xs_offset = static_cast<int>(at);
-  at += slice * 256 * p.cols;
+  at += x_cols * column;
   a->red_offset = static_cast<int>(at);
-  if (p.team > 1 || p.split > 1) at += int64_t{2} * p.warps * p.cols * 16 * p.r * 4;
+  at += red;
+  a->acc_offset = static_cast<int>(at);
+  at += acc;
   a->ids_offset = static_cast<int>(at);
-  if (experts) at += (int64_t{2} * pairs + 15) / 16 * 16;
+  at += ids;
   a->smem_bytes = static_cast<int>(at);
-  return at;
+  return true;
 }
 
 static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
@@ -84,18 +104,14 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
     // Each set has an expert of its own or is full.
     p->sets = experts ? a->E + a->pairs / p->cols : (a->pairs + p->cols - 1) / p->cols;
     if (p->sets > a->pairs) p->sets = a->pairs;
-    for (p->r = 2; p->r >= 1; p->r /= 2) {
+    for (p->r = group == 32 ? 1 : 2; p->r >= 1; p->r /= 2) {
       if (p->r > 1 && p->sets * ((a->N + 16 * p->r - 1) / (16 * p->r)) < 4 * sms) continue;
-      for (p->warps = 16; p->warps >= 8; p->warps /= 2)
-        for (p->split = 1; p->split <= 8 && p->split <= a->units; p->split *= 2) {
-          const int slice = (a->units + p->split - 1) / p->split;
-          p->team = 1;
-          while (p->team < p->warps && slice >= 4 * p->team) p->team *= 2;
-          const int64_t bytes = w4_layout(*p, group, a->units, a->pairs, experts, a);
-          if (bytes > most) continue;
-          p->ctas_per_sm = 1;
-          return true;
-        }
+      p->warps = 16;
+      p->team = a->units >= 48 ? 16 : a->units >= 16 ? 4 : 1;
+      for (int phases = 1; phases <= a->units; ++phases) {
+        p->phase_units = (a->units + phases - 1) / phases;
+        if (w4_layout(p, group, most, experts, a)) return true;
+      }
     }
   }
   return false;
@@ -130,7 +146,7 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   DeviceState *d = current_device(&st);
   if (!d) return st;
   // Dynamic shared memory beside the kernels' own (the experts' tables).
-  const int64_t most = d->smem_optin - 4096;
+  const int64_t most = d->smem_optin - 8192;
   st = allow_shared_memory(static_cast<int>(most));
   if (st != AR_OK) return st;
   W4Args a = {};
@@ -140,32 +156,33 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.scales = static_cast<const uint8_t *>(scales);
   a.zeros = static_cast<const uint8_t *>(zeros);
   a.out = static_cast<__nv_bfloat16 *>(out);
-  a.scale_count = E * N * ng;
   a.pairs = static_cast<int>(pairs);
   a.k = x_per_pair ? 1 : k;
   a.E = E;
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
   a.ng = static_cast<int>(ng);
+  a.scale_count = E * N * ng;
   a.width = static_cast<int>(width);
   a.act = act;
-  a.scale_type = scales_type;
   a.units = static_cast<int>((K + kW4UnitK - 1) / kW4UnitK);
   a.status = d->status;
 
   W4Plan p;
   if (!w4_plan(m, experts, group, most, d->sms, &a, &p)) return AR_ERR_UNSUPPORTED;
   a.cols = p.cols;
-  a.split = p.split;
+  a.x_cols = p.x_cols;
+  a.warps = p.warps;
   a.team = p.team;
+  a.phase_units = p.phase_units;
+  a.wait_limit_ns = kWaitLimitNs;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
   a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
-  int64_t clusters = p.sets * a.row_blocks;
-  const int64_t cap = int64_t{d->sms} * p.ctas_per_sm / p.split;
-  if (clusters > cap) clusters = cap;
+  int64_t ctas = p.sets * a.row_blocks;
+  if (ctas > d->sms) ctas = d->sms;
   const W4Kernel kern = w4_kernel(scales_type, zeros != nullptr, experts, p.r, p.nt, group);
-  return launch_pdl(kern, a, clusters * p.split, p.warps * 32, static_cast<size_t>(a.smem_bytes),
-                    p.split, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_pdl(kern, a, ctas, p.warps * 32, static_cast<size_t>(a.smem_bytes), 1,
+                    static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? AR_OK
              : AR_ERR_CUDA;
 }

@@ -40,13 +40,20 @@
 // load where the group allows it.  The row stride (112, 96, 64 bytes) keeps
 // each of these free of bank conflicts.  The pairs of a word come out as
 // (i, i + 4), so x is stored with its eights in that order, in the order of
-// the lanes.
+// the lanes.  (One warp that feeds all rings by tensor-map copies was
+// measured and dropped: 70 ns a 2 KB box, where memory brings one in 45.)
 //
 // Work.  An item is 16 R rows x one column set (an expert's tokens, up to
-// 8 NT).  A cluster of S CTAs takes a contiguous range of items, CTA q of it
-// the units q, q + S, ... of each.  A CTA's warps form teams: a team takes
-// items of the range in turn, and its warps the units of an item in turn.
-// The ring runs on across items.
+// 8 NT).  A CTA takes a contiguous range of items, its warps form teams, a
+// team takes items of the range in turn, and its warps the units of the
+// team's items in turn, whatever item they belong to: all warps do the same
+// number of units, and the ring runs on across items.  A warp that ends an
+// item leaves its sums in shared memory, goes on, and adds up its part of
+// the item before once every warp of the team has left that one (mbarriers,
+// bounded waits); a team of one needs none of this.  x of as many column
+// sets as fit is unpacked into shared memory at once.  Where not even one
+// set fits, the range is walked in phases, a part of K in each, and the sums
+// so far wait in shared memory.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -55,7 +62,7 @@
 
 namespace arn {
 
-constexpr int kW4MaxWarps = 16;
+constexpr int kW4MaxWarps = 16;  // four a scheduler, 128 registers a thread
 constexpr int kW4UnitK = 128;  // k of a unit
 
 struct W4Args {
@@ -71,20 +78,24 @@ struct W4Args {
   int E, N, K, ng;  // ng: groups of a row
   int width;        // columns of out: N, or N / 2 with the gated activation
   int act;
-  int scale_type;
   int units;        // units of a row: ceil(K / 128)
   int row_blocks;   // items of a column set
   int cols;         // most columns of a set
-  int split;        // CTAs of a cluster
-  int team;         // warps of a team
-  int xs_offset, red_offset, ids_offset;  // shared memory
+  int x_cols;       // columns of x that shared memory holds (at least cols)
+  int warps, team;  // of a CTA, of a team
+  int phase_units;  // units of a phase; all of them: one phase
+  int phase_rounds; // items a team walks per phase (several phases)
+  int xs_offset, red_offset, acc_offset, ids_offset;  // shared memory
   int smem_bytes;
+  uint64_t wait_limit_ns;
   int *status;
 };
 
-// Units of a warp's ring: two to five in flight behind the one in use, 64 KB
-// or more an SM with the plan's warps.
-__host__ __device__ constexpr int w4_depth(int r) { return r == 1 ? 6 : 3; }
+constexpr int kW4MaxSets = 32;   // column sets staged at a time
+constexpr int kW4MaxXCols = 64;  // columns staged at a time
+
+// Units of a warp's ring: 64 KB in flight an SM behind those in use.
+__host__ __device__ constexpr int w4_depth(int r) { return r == 1 ? 5 : 3; }
 __host__ __device__ constexpr int w4_row_bytes(int group) {
   return group == 32 ? 112 : group == 64 ? 96 : 64;
 }
@@ -94,11 +105,18 @@ __host__ __device__ constexpr int w4_slot_bytes(int r, int group) {
   return 16 * r * (w4_row_bytes(group) + (group == 128 ? 8 : 0));
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first `bytes` of the source, zeros behind them (some instructions more).
+__device__ __forceinline__ void cp_async_16_of(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, uint32_t bytes) {
+__device__ __forceinline__ void cp_async_4_of(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
@@ -146,7 +164,7 @@ __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
 // Weights i and i + 4 of a word, i = 0 .. 3, less the zero point.
 __device__ __forceinline__ void unpack_word(uint32_t (&p)[4], uint32_t word, const Offsets &o) {
-  const __half2 sixteenth = as_half2(0x2C002C00u);
+  const __half2 sixteenth = as_half2(0x2C002C00u);  // 1/16
   const uint32_t next = word >> 8;
   p[0] = as_bits(__hadd2(as_half2(and_or(word, 0x000F000Fu, 0x64006400u)), as_half2(o.low)));
   p[1] = as_bits(__hfma2(as_half2(and_or(word, 0x00F000F0u, 0x64006400u)), sixteenth,
@@ -220,30 +238,76 @@ __device__ __forceinline__ void prefetch_line(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(const float *local, uint32_t rank) {
-  uint32_t at;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ float gated(float gate, float up) {
   return gate / (1.f + expf(-gate)) * up;
 }
 
-// Row of W behind local row lr of block b.  Local rows come in sixteens;
-// with the gated activation the first eight are gate rows and the last eight
-// the up rows of the same outputs.  Beyond the end: the last row, whose
-// result is not stored.
+// Row of W behind local row lr of block b: with the gated activation the
+// first 8 R are gate rows, the others the up rows of the same outputs.
+// Beyond the end: the last row, whose result is not stored.
 template <int R>
 __device__ __forceinline__ int w4_row(const W4Args &a, int block, int lr) {
   if (a.act == AR_ACT_SILU_MUL) {
-    const int o = block * 8 * R + (lr >> 4) * 8 + (lr & 7);
-    return min(o, a.width - 1) + ((lr >> 3) & 1) * a.width;
+    const int half = lr >= 8 * R ? 1 : 0;
+    return min(block * 8 * R + lr - half * 8 * R, a.width - 1) + half * a.width;
   }
   return min(block * 16 * R + lr, a.N - 1);
 }
+
+// A warp's way through its CTA's items [item0, item1): chunk by chunk, in
+// each chunk phase by phase, in each phase the team's items, and of all their
+// units in a row every team'th.  One phase: one chunk.
+struct W4Walk {
+  int item1, teams, team_warps, team, member;
+  int base, end;   // the chunk
+  int u0, u1;      // the phase's units
+  int item, unit;  // where the warp is
+  bool more;
+
+  __device__ __forceinline__ int chunk_end(const W4Args &a, int first) const {
+    if (a.phase_units >= a.units) return item1;
+    const int set_end = (first / a.row_blocks + 1) * a.row_blocks;
+    return min(item1, min(set_end, first + a.phase_rounds * teams));
+  }
+  __device__ __forceinline__ void start(const W4Args &a, int item0, int item1_, int warp) {
+    item1 = item1_;
+    team_warps = a.team;
+    teams = a.warps / a.team;
+    team = warp / a.team;
+    member = warp % a.team;
+    base = item0;
+    end = chunk_end(a, item0);
+    u0 = 0;
+    u1 = a.phase_units;
+    item = base + team;
+    unit = member;
+    more = item0 < item1;
+    if (more) settle(a);
+  }
+  // From (item, unit) on, the first unit that exists.
+  __device__ __forceinline__ void settle(const W4Args &a) {
+    for (;;) {
+      if (item >= end) {  // next phase, or next chunk
+        u0 = u1;
+        if (u0 >= a.units) {
+          u0 = 0;
+          base = end;
+          more = base < item1;
+          if (!more) return;
+          end = chunk_end(a, base);
+        }
+        u1 = min(a.units, u0 + a.phase_units);
+        item = base + team;
+        unit = u0 + member;
+      } else if (unit >= u1) {  // the team's warps take up the next item where this one left them
+        unit -= u1 - u0;
+        item += teams;
+      } else {
+        return;
+      }
+    }
+  }
+};
 
 // ST: AR_TYPE_* of the scales; ZEROS: whether there are zero points.
 template <int R, int NT, int G, int ST, bool ZEROS, bool EXPERTS>
@@ -263,39 +327,44 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   constexpr int kScaleWords = ST == AR_TYPE_F32 ? kGroups : kGroups == 1 ? 1 : kGroups / 2 + 1;
   constexpr int kZeroWords = kGroups == 1 ? 1 : 2;
 
-  const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int S = a.split;
-  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int cluster_id = static_cast<int>(blockIdx.x) / S, clusters = static_cast<int>(gridDim.x) / S;
-  const int units = (a.units - rank + S - 1) / S;  // this CTA's units of an item
+  const int warps = a.warps, threads = warps * 32;
   const int teams = warps / a.team, team = warp / a.team, member = warp % a.team;
-  const int64_t row_bytes = a.K / 2;
 
-  unsigned char *ring = w4_smem + warp * (kDepth * kSlot);
+  const uint32_t ring = smem_addr(w4_smem) + warp * (kDepth * kSlot);
   uint4 *xs = reinterpret_cast<uint4 *>(w4_smem + a.xs_offset);
+  // red[team][item & 1][member][column][row], sums[round of the phase][team][column][row]
   float *red = reinterpret_cast<float *>(w4_smem + a.red_offset);
+  float *sums = reinterpret_cast<float *>(w4_smem + a.acc_offset);
+  const int tile = a.cols * kRows;  // sums of an item
 
   // Experts: ids16[p] the expert of pair p (-1: none), sets[e] the number of
-  // column sets before expert e.
+  // column sets before expert e, counts[e] its pairs.
   int16_t *ids16 = reinterpret_cast<int16_t *>(w4_smem + a.ids_offset);
   __shared__ int sets[EXPERTS ? AR_MAX_EXPERTS + 1 : 1];
-  __shared__ int col_pair[8 * NT];
-  __shared__ int col_count;
-  __shared__ int col_top[8 * NT];  // bits of a column's largest finite |x|
-  __shared__ uint4 zero16;
+  __shared__ int16_t counts[EXPERTS ? AR_MAX_EXPERTS : 1];
+  // The staged sets: expert, first column, columns.
+  __shared__ int set_expert[kW4MaxSets], set_col[kW4MaxSets + 1];
+  __shared__ int set_count;
+  __shared__ int col_pair[kW4MaxXCols];
+  __shared__ int col_top[kW4MaxXCols];  // bits of a column's largest finite |x|
+  __shared__ uint4 nothing[20];         // a unit of no column: zeros
+  // Of team and buffer: all warps have left their sums, all have read them.
+  __shared__ uint64_t full[kW4MaxWarps], empty[kW4MaxWarps];
+  __shared__ int aborted;
 
   int nsets = (a.pairs + a.cols - 1) / a.cols;
   if constexpr (!EXPERTS) {
     // The first units' lines on their way to L2 while the previous grid
     // drains: nothing enters this SM before the wait.
     const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
-    const int64_t item = total * cluster_id / clusters + team;
-    if (item < total * (cluster_id + 1) / clusters && (t & 1) == 0) {
+    const int64_t item = total * blockIdx.x / gridDim.x + team;
+    if (item < total * (blockIdx.x + 1) / gridDim.x && (t & 1) == 0) {
       const int block = static_cast<int>(item % a.row_blocks);
-      for (int d = 0, lu = member; d < kDepth - 1 && lu < units; ++d, lu += a.team) {
-        const int64_t piece = static_cast<int64_t>(lu * S + rank) * 64 + t * 16;
+      const int64_t row_bytes = a.K / 2;
+      for (int d = 0, u = member; d < kDepth - 1 && u < a.phase_units; ++d, u += a.team) {
+        const int64_t piece = static_cast<int64_t>(u) * 64 + t * 16;
 #pragma unroll
         for (int i = 0; i < 2 * R; ++i)
           if (piece < row_bytes)
@@ -303,11 +372,18 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       }
     }
   }
+  if (tid < kW4MaxWarps) {
+    mbar_init(&full[tid], a.team);
+    mbar_init(&empty[tid], a.team);
+  }
+  if (tid < 20) nothing[tid] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) aborted = 0;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
   if constexpr (EXPERTS) {
-    for (int e = tid; e <= AR_MAX_EXPERTS; e += threads) sets[e] = 0;
+    const int each = (a.E + 31) / 32;  // experts a lane counts up
+    for (int e = tid; e < 32 * each; e += threads) sets[e] = 0;
     __syncthreads();
     for (int p = tid; p < a.pairs; p += threads) {
       const int e = __ldg(a.ids + p);
@@ -317,39 +393,47 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     }
     __syncthreads();
     if (warp == 0) {  // counts -> column sets before each expert
-      constexpr int kEach = AR_MAX_EXPERTS / 32;
       int mine = 0;
-      for (int i = 0; i < kEach; ++i) mine += (sets[lane * kEach + i] + a.cols - 1) / a.cols;
+      for (int i = 0; i < each; ++i) mine += (sets[lane * each + i] + a.cols - 1) / a.cols;
       int before = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
         if (lane >= o) before += v;
       }
-      if (lane == 31) sets[AR_MAX_EXPERTS] = before;
+      const int all = __shfl_sync(0xFFFFFFFFu, before, 31);
       before -= mine;
-      for (int i = 0; i < kEach; ++i) {
-        const int n = (sets[lane * kEach + i] + a.cols - 1) / a.cols;
-        sets[lane * kEach + i] = before;
-        before += n;
+      __syncwarp();
+      for (int i = 0; i < each; ++i) {
+        const int e = lane * each + i;
+        if (e < a.E) {
+          const int n = sets[e];
+          counts[e] = static_cast<int16_t>(n);
+          sets[e] = before;
+          before += (n + a.cols - 1) / a.cols;
+        }
       }
+      __syncwarp();
+      if (lane == 0) sets[a.E] = all;
     }
     __syncthreads();
-    nsets = sets[AR_MAX_EXPERTS];
+    nsets = sets[a.E];
     // Pairs without an expert here: zero rows, spread over the grid.
     for (int p = blockIdx.x; p < a.pairs; p += gridDim.x)
       if (ids16[p] < 0)
         for (int n = tid; n < a.width; n += threads)
           a.out[static_cast<int64_t>(p) * a.width + n] = __float2bfloat16_rn(0.f);
+  } else {
+    __syncthreads();  // the barriers are there
   }
   const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
-  const int item0 = static_cast<int>(total * cluster_id / clusters);
-  const int item1 = static_cast<int>(total * (cluster_id + 1) / clusters);
+  const int item0 = static_cast<int>(total * blockIdx.x / gridDim.x);
+  const int item1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
 
   // The expert of a column set.
   auto expert_of = [&](int set) -> int {
     if constexpr (!EXPERTS) return 0;
-    int lo = 0, hi = AR_MAX_EXPERTS;  // sets[lo] <= set < sets[hi]
+    int lo = 0, hi = a.E;  // sets[lo] <= set < sets[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sets[mid] <= set) lo = mid;
@@ -358,376 +442,446 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     return lo;
   };
 
-  // The fetching side of the ring.  f_item: the team's item, f_base and
-  // f_end: the column set's part of the range.
-  int f_item = item0 + team, f_base = item0, f_end = item0, f_unit = member, f_slot = 0;
-  int f_block0 = 0;              // block of f_base
+  const bool act = a.act == AR_ACT_SILU_MUL;
+  const int outs = act ? 8 * R : kRows;  // outputs of an item's column
+
+  // The fetching side of the ring, `to_come` units of an item at a time.
+  W4Walk walk;
+  walk.start(a, item0, item1, warp);
+  const int64_t row_bytes = a.K / 2;
+  int to_come = 0, f_unit = 0;
+  int f_set = -1;
   int64_t f_first = 0;           // first row of W of the set's expert
-  const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the expert's first row
+  const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the unit in the expert's first row
   uint32_t f_off[2 * R];         // the rows' distances, in 16 bytes
-  const uint8_t *f_s = nullptr, *f_z = nullptr;  // scales and zero points of row `lane`
-  bool f_tail = false;           // near the end of their arrays
-  const int full_units = static_cast<int>(row_bytes >> 6);  // units of a row that are whole
-  auto next_item = [&]() {       // from f_item on, the team's first item that exists
-    if (f_item >= f_end) {
-      while (f_item >= f_end && f_end < item1) {
-        f_base = f_end;
-        f_item = f_base + team;
-        const int set = f_base / a.row_blocks;
-        f_block0 = f_base - set * a.row_blocks;
-        f_end = min(item1, f_base - f_block0 + a.row_blocks);
-        f_first = static_cast<int64_t>(expert_of(set)) * a.N;
-      }
-      if (f_item >= f_end) return;
-      f_q = a.q + f_first * row_bytes + t * 16;
+  const uint8_t *f_s = nullptr, *f_z = nullptr;  // the unit's scales and zero points of row `lane`
+  bool f_plain = false;          // neither ends inside a unit nor near the end of its arrays
+  uint32_t f_slot = ring;
+  // Points at the rows of the walk's item and takes its units.
+  auto next_item = [&]() {
+    const int set = walk.item / a.row_blocks, block = walk.item - set * a.row_blocks;
+    if (set != f_set) {
+      f_set = set;
+      f_first = static_cast<int64_t>(expert_of(set)) * a.N;
     }
-    const int block = f_item - f_base + f_block0;
+    f_unit = walk.unit;
+    to_come = (walk.u1 - walk.unit + a.team - 1) / a.team;
+    f_q = a.q + f_first * row_bytes + t * 16 + f_unit * 64;
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i)
       f_off[i] = static_cast<uint32_t>(w4_row<R>(a, block, g + 8 * i)) *
                  static_cast<uint32_t>(row_bytes >> 4);
-    const int64_t el = (f_first + w4_row<R>(a, block, lane & (kRows - 1))) * a.ng;
+    const int64_t el = (f_first + w4_row<R>(a, block, lane & (kRows - 1))) * a.ng + f_unit * kGroups;
     f_s = a.scales + el * kScaleBytes;
     if constexpr (ZEROS) f_z = a.zeros + el;
-    f_tail = el + a.ng + 16 > a.scale_count;
+    f_plain = __all_sync(0xFFFFFFFFu, el + a.ng + 16 <= a.scale_count) && a.K % kW4UnitK == 0;
+    walk.unit += to_come * a.team;
+    walk.settle(a);
   };
-  next_item();
+  auto word_of = [](const uint8_t *p) -> const uint8_t * {
+    return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t{3});
+  };
   auto fetch = [&]() {
-    while (f_item < f_end && f_unit >= units) {
-      // The team's warps take up the next item where this one left them.
-      f_unit -= units;
-      f_item += teams;
-      next_item();
-    }
-    if (f_item < f_end) {
-      const int u = f_unit * S + rank;
-      const uint32_t slot = smem_addr(ring) + f_slot * kSlot;
-      const uint32_t to = slot + g * kRowBytes + t * 16;
-      if (u < full_units) {
-        const uint8_t *src = f_q + u * 64;
+    if (to_come == 0 && walk.more) next_item();
+    if (to_come > 0) {
+      --to_come;
+      const uint32_t to = f_slot + g * kRowBytes + t * 16;
+      const uint32_t to_s = f_slot + kScaleAt + lane * kScaleStride;
+      const uint8_t *ws = word_of(f_s), *wz = word_of(f_z);
+      if (f_plain) {
 #pragma unroll
         for (int i = 0; i < 2 * R; ++i)
-          cp_async_16(to + 8 * i * kRowBytes, src + static_cast<uint64_t>(f_off[i]) * 16, 16u);
-      } else {  // the row ends inside the unit: zeros behind it
-        const bool here = u * 64 + t * 16 < static_cast<int>(row_bytes);
-        const uint8_t *src = f_q + (here ? u * 64 : 0);
+          cp_async_16(to + 8 * i * kRowBytes, f_q + static_cast<uint64_t>(f_off[i]) * 16);
+        if (kRows == 32 || lane < kRows) {
+#pragma unroll
+          for (int i = 0; i < kScaleWords; ++i) cp_async_4(to_s + 4 * i, ws + 4 * i);
+          if constexpr (ZEROS) {
+#pragma unroll
+            for (int i = 0; i < kZeroWords; ++i) cp_async_4(to_s + kZeroAt + 4 * i, wz + 4 * i);
+          }
+        }
+      } else {
+        // Zeros behind the row's end; words cut off at the end of the arrays.
+        const bool here = f_unit * 64 + t * 16 < static_cast<int>(row_bytes);
 #pragma unroll
         for (int i = 0; i < 2 * R; ++i)
-          cp_async_16(to + 8 * i * kRowBytes, src + static_cast<uint64_t>(f_off[i]) * 16,
-                      here ? 16u : 0u);
-      }
-      // The aligned words around the unit's scales and zero points, cut off
-      // at the end of their arrays.
-      if (lane < kRows) {
-        const uint32_t to_s = slot + kScaleAt + lane * kScaleStride;
-        auto words = [&](uint32_t dst, const uint8_t *p, const uint8_t *end, int n) {
-          const uint8_t *w = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) &
-                                                               ~uintptr_t{3});
-          if (!f_tail) {
-#pragma unroll
-            for (int i = 0; i < n; ++i) cp_async_4(dst + 4 * i, w + 4 * i, 4u);
-          } else {
-#pragma unroll
+          cp_async_16_of(to + 8 * i * kRowBytes,
+                         here ? f_q + static_cast<uint64_t>(f_off[i]) * 16 : a.q, here ? 16u : 0u);
+        if (lane < kRows) {
+          auto words = [&](uint32_t dst, const uint8_t *w, const uint8_t *end, int n) {
             for (int i = 0; i < n; ++i) {
               const int64_t left = end - (w + 4 * i);
               if (left > 0)
-                cp_async_4(dst + 4 * i, w + 4 * i, left < 4 ? static_cast<uint32_t>(left) : 4u);
+                cp_async_4_of(dst + 4 * i, w + 4 * i, left < 4 ? static_cast<uint32_t>(left) : 4u);
             }
-          }
-        };
-        words(to_s, f_s + u * (kGroups * kScaleBytes), a.scales + a.scale_count * kScaleBytes,
-              kScaleWords);
-        if constexpr (ZEROS)
-          words(to_s + kZeroAt, f_z + u * kGroups, a.zeros + a.scale_count, kZeroWords);
+          };
+          words(to_s, ws, a.scales + a.scale_count * kScaleBytes, kScaleWords);
+          if constexpr (ZEROS) words(to_s + kZeroAt, wz, a.zeros + a.scale_count, kZeroWords);
+        }
       }
-      f_slot = f_slot + 1 == kDepth ? 0 : f_slot + 1;
       f_unit += a.team;
+      f_q += a.team * 64;
+      f_s += a.team * (kGroups * kScaleBytes);
+      if constexpr (ZEROS) f_z += a.team * kGroups;
+      f_slot += kSlot;
+      if (f_slot == ring + kDepth * kSlot) f_slot = ring;
     }
     cp_async_commit();  // an empty group at the end keeps the count
   };
 #pragma unroll 1
   for (int i = 0; i < kDepth - 1; ++i) fetch();
 
-  const bool act = a.act == AR_ACT_SILU_MUL;
-  const int outs = act ? 8 * R : kRows;  // outputs of an item's column
-  int c_unit = member, slot_at = 0, parity = 0;
-#pragma unroll 1
-  for (int seg = item0; seg < item1;) {
-    // The part of the range that has one column set.
-    const int set = seg / a.row_blocks;
-    const int seg_end = min(item1, (set + 1) * a.row_blocks);
-    const int expert = expert_of(set);
-    __syncthreads();  // nobody uses the last set's x any more
-    if (tid == 0) zero16 = make_uint4(0, 0, 0, 0);
-    if (tid < 8 * NT) col_top[tid] = 0;
-    if constexpr (EXPERTS) {
-      if (warp == 0) {  // the set's columns, in the order of the pairs
-        const int skip = (set - sets[expert]) * a.cols;
-        int seen = 0;
-        for (int p0 = 0; p0 < a.pairs && seen < skip + a.cols; p0 += 32) {
-          const bool is = p0 + lane < a.pairs && ids16[p0 + lane] == expert;
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
-          const int at = seen + __popc(who & ((1u << lane) - 1u)) - skip;
-          if (is && at >= 0 && at < a.cols) col_pair[at] = p0 + lane;
-          seen += __popc(who);
+  // Units [u0, u1) of the first n columns into shared memory, as fp16 times
+  // their powers of two: [unit][column][step][lane], odd columns with the
+  // steps of a pair exchanged (no bank conflicts between two columns).
+  auto stage = [&](int u0, int u1, int n) {
+    const int pieces = (u1 - u0) * 16;  // eights of a column
+    auto place = [&](int i, int *col) -> uint4 * {  // of eight i of all columns
+      *col = i / pieces;
+      const int j = i - *col * pieces, to = step_lane<G>(j & 15);
+      return xs + ((j >> 4) * a.x_cols + *col) * 16 + (to ^ ((*col & 1) << 2));
+    };
+    for (int i0 = 0; i0 < pieces * n; i0 += threads) {
+      // Sixteen lanes hold eights of one column.
+      const int i = i0 + tid;
+      int col, top = 0;
+      uint4 *to = place(i, &col);
+      if (col < n) {
+        const int at = u0 * 16 + i - col * pieces;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (at * 8 < a.K)
+          w = __ldg(a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + at);
+        float f[8];
+        unpack8(w, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int bits = __float_as_int(f[e]) & 0x7FFFFFFF;
+          if (bits < 0x7F800000 && bits > top) top = bits;
         }
-        if (lane == 0) col_count = min(seen - skip, a.cols);
+        *to = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
+                         __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
       }
-    } else {
-      const int n = min(a.cols, a.pairs - set * a.cols);
-      if (tid < n) col_pair[tid] = set * a.cols + tid;
-      if (tid == 0) col_count = n;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      if ((lane & 15) == 0 && col < n && top > 0) atomicMax(&col_top[col], top);
     }
     __syncthreads();
-    const int ncols = col_count;
-    {
-      const int pieces = units * 16;  // eights of a column
-      auto place = [&](int i, int *col) -> uint4 * {  // of eight i of all columns
-        *col = i / pieces;
-        const int j = i - *col * pieces, to = step_lane<G>(j & 15);
-        return xs + (((j >> 4) * 4 + (to >> 2)) * a.cols + *col) * 4 + (to & 3);
-      };
-      for (int i0 = 0; i0 < pieces * ncols; i0 += threads) {
-        // Sixteen lanes hold eights of one column.
-        const int i = i0 + tid;
-        int col, top = 0;
-        uint4 *to = place(i, &col);
-        if (col < ncols) {
-          const int j = i - col * pieces, at = ((j >> 4) * S + rank) * 16 + (j & 15);
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (at * 8 < a.K)
-            w = __ldg(a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + at);
-          float f[8];
-          unpack8(w, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int bits = __float_as_int(f[e]) & 0x7FFFFFFF;
-            if (bits < 0x7F800000 && bits > top) top = bits;
-          }
-          *to = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
-                           __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if ((lane & 15) == 0 && col < ncols && top > 0) atomicMax(&col_top[col], top);
-      }
-      __syncthreads();
-      for (int i = tid; i < pieces * ncols; i += threads) {  // what this thread has put there
-        int col;
-        uint4 *to = place(i, &col);
-        const float down = __int_as_float((127 - exponent_of(col_top[col])) << 23);
-        uint4 v = *to;
-        v.x = halves_of(v.x, down), v.y = halves_of(v.y, down);
-        v.z = halves_of(v.z, down), v.w = halves_of(v.w, down);
-        *to = v;
-      }
+    for (int i = tid; i < pieces * n; i += threads) {  // what this thread has put there
+      int col;
+      uint4 *to = place(i, &col);
+      const float down = __int_as_float((127 - exponent_of(col_top[col])) << 23);
+      uint4 v = *to;
+      v.x = halves_of(v.x, down), v.y = halves_of(v.y, down);
+      v.z = halves_of(v.z, down), v.w = halves_of(v.w, down);
+      *to = v;
     }
     __syncthreads();
+  };
 
-    // This lane's eights of x: column g of each tile, or zeros.  And where
-    // its two columns of each tile's sums go.
-    uint32_t xp[NT], xstep[NT];
-    __nv_bfloat16 *op[NT][2];
-    float up[NT][2];  // the columns' powers of two
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const bool in = n * 8 + g < ncols;
-      xp[n] = in ? smem_addr(xs + (n * 8 + g) * 4 + t) : smem_addr(&zero16);
-      xstep[n] = in ? a.cols * 64 : 0;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = n * 8 + 2 * t + c;
-        up[n][c] = __int_as_float((127 + exponent_of(col_top[col])) << 23);
-        op[n][c] = col < ncols ? a.out + static_cast<int64_t>(col_pair[col]) * a.width : nullptr;
+  int done = 0;  // items of this team that its warps have left (its buffers' phases)
+  struct Item {
+    int block, col, ncols, round;
+  };
+  // This warp's part of adding up item `it`, the team's number `n`, once
+  // every warp has left its sums.
+  auto gather = [&](const Item &it, int n, bool first, bool last) {
+    const int at = team * 2 + (n & 1);
+    mbar_wait_bounded(&full[at], (n >> 1) & 1, &aborted, a.wait_limit_ns, a.status);
+    const float *buf = red + at * a.team * tile;
+    float *sum = sums + (it.round * teams + team) * tile;
+    auto sum_of = [&](int col, int row) -> float {
+      const float *p = buf + col * kRows + row;
+      float v = p[0];
+      for (int w = 1; w < a.team; ++w) v += p[w * tile];
+      if (!first) v += sum[col * kRows + row];
+      if (!last) sum[col * kRows + row] = v;
+      return v;
+    };
+    for (int i = member * 32 + lane; i < it.ncols * outs; i += a.team * 32) {
+      const int col = i / outs, o = i - col * outs;
+      float v = sum_of(col, o);
+      if (act) {
+        const float up = sum_of(col, o + 8 * R);
+        if (last) v = gated(v, up);
       }
+      const int n0 = it.block * outs + o;
+      if (last && n0 < a.width)
+        a.out[static_cast<int64_t>(col_pair[it.col + col]) * a.width + n0] = __float2bfloat16_rn(v);
     }
-    const int rounds = (seg_end - seg + teams - 1) / teams;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[at]);
+  };
+
+  uint32_t slot = ring;
 #pragma unroll 1
-    for (int round = 0; round < rounds; ++round) {
-      const int item = seg + round * teams + team;
-      const bool has = item < seg_end;
-      const int block = item - set * a.row_blocks;
-      float acc[R][NT][4];
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[r][n][c] = 0.f;
-      if (has) {
-        int el_low[R][2];  // low bits of the rows' first group numbers
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            el_low[r][h] =
-                ((expert * a.N + w4_row<R>(a, block, r * 16 + h * 8 + g)) & 3) * (a.ng & 3);
+  for (int base = item0; base < item1;) {
+    const int chunk = walk.chunk_end(a, base);  // depends on base alone
+    for (int u0 = 0; u0 < a.units; u0 += a.phase_units) {
+      const int u1 = min(a.units, u0 + a.phase_units), nunits = u1 - u0;
+      const bool first = u0 == 0, last = u1 == a.units;
+      int c_unit = member;           // of the phase
+      int item = base + team, round = 0;
+      Item left = {0, 0, 0, 0};      // the team's item before, not added up yet
+      bool pending = false;
 #pragma unroll 1
-        for (; c_unit < units; c_unit += a.team) {
-          cp_async_wait<kDepth - 2>();
-          __syncwarp();  // every lane's copies are here, and the slot before is free
-          fetch();
-          const uint32_t slot = smem_addr(ring) + slot_at * kSlot;
-          slot_at = slot_at + 1 == kDepth ? 0 : slot_at + 1;
-          uint4 b[4][NT];
+      for (int at = base; at < chunk;) {
+        // The column sets from item `at` on that fit together: [at, end).
+        const int set0 = at / a.row_blocks;
+        __syncthreads();  // nobody uses the sets before any more
+        if (warp == 0) {
+          const int set = set0 + lane;
+          const bool there = set < nsets && set * a.row_blocks < chunk;
+          int n = 0;
+          if (there) {
+            const int e = expert_of(set);
+            if constexpr (EXPERTS) n = min(a.cols, counts[e] - (set - sets[e]) * a.cols);
+            else n = min(a.cols, a.pairs - set * a.cols);
+            set_expert[lane] = e;
+          }
+          int before = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (lane >= o) before += v;
+          }
+          const uint32_t fit = __ballot_sync(0xFFFFFFFFu, there && before <= a.x_cols);
+          if (lane == 0) {
+            set_count = __popc(fit);
+            set_col[0] = 0;
+          }
+          if (fit >> lane & 1u) set_col[lane + 1] = before;
+        }
+        for (int c = tid; c < kW4MaxXCols; c += threads) col_top[c] = 0;
+        __syncthreads();
+        const int count = set_count;
+        const int end = min(chunk, (set0 + count) * a.row_blocks);
+        for (int i = warp; i < count; i += warps) {  // the sets' pairs, in order
+          const int c0 = set_col[i], n = set_col[i + 1] - c0;
+          if constexpr (EXPERTS) {
+            const int e = set_expert[i], skip = (set0 + i - sets[e]) * a.cols;
+            int seen = 0;
+            for (int p0 = 0; p0 < a.pairs && seen < skip + n; p0 += 32) {
+              const bool is = p0 + lane < a.pairs && ids16[p0 + lane] == e;
+              const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
+              const int k = seen + __popc(who & ((1u << lane) - 1u)) - skip;
+              if (is && k >= 0 && k < n) col_pair[c0 + k] = p0 + lane;
+              seen += __popc(who);
+            }
+          } else {
+            if (lane < n) col_pair[c0 + lane] = (set0 + i) * a.cols + lane;
+          }
+        }
+        __syncthreads();
+        stage(u0, u1, set_col[count]);
+
+#pragma unroll 1
+        for (; item < end; item += teams, ++round) {
+          const int set = item / a.row_blocks, si = set - set0;
+          const Item it = {item - set * a.row_blocks, set_col[si], set_col[si + 1] - set_col[si], round};
+          // This lane's eights of x: column g of each tile, or zeros; even
+          // and odd steps.
+          uint32_t xe[NT], xo[NT], xstep[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint32_t p = xp[n] + c_unit * 4 * xstep[n];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i][n] = lds_128(p + i * xstep[n]);
+            const int col = it.col + n * 8 + g;
+            const bool in = n * 8 + g < it.ncols;
+            const uint32_t p = in ? smem_addr(xs + col * 16 + t) : smem_addr(nothing + 4);
+            const int odd = in ? (col & 1) * 64 : 0;
+            xe[n] = p + odd;
+            xo[n] = p - odd;
+            xstep[n] = in ? a.x_cols * 256 : 0;
           }
-          const int u0 = (c_unit * S + rank) * kGroups;
+          // Low bits of the rows' first group numbers.
+          const int first_row = set_expert[si] * a.N;
+          int el_low[R][2];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t row = slot + (r * 16 + g) * kRowBytes;
-            uint32_t w0[4], w1[4];
-            load_words<G>(w0, row, t);
-            load_words<G>(w1, row + 8 * kRowBytes, t);
-            const uint32_t sc = slot + kScaleAt + (r * 16 + g) * kScaleStride;
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-              // Scale and zero point of the two rows' group.
-              float s[2];
-              Offsets o[2];
+            for (int h = 0; h < 2; ++h)
+              el_low[r][h] =
+                  ((first_row + w4_row<R>(a, it.block, r * 16 + h * 8 + g)) & 3) * (a.ng & 3);
+          float acc[R][NT][4];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t p = sc + h * 8 * kScaleStride;
-                const int low = el_low[r][h] + u0;
-                if constexpr (ST == AR_TYPE_F32) {
-                  s[h] = __uint_as_float(lds_32(p + gi * 4));
-                } else {
-                  const uint32_t v = lds_16(p + ((low & 1) + gi) * 2);
-                  s[h] = ST == AR_TYPE_BF16
-                             ? __uint_as_float(v << 16)
-                             : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
-                }
-                // Behind the row's end stands another row's scale.
-                if (kGroups > 1 && u0 + gi >= a.ng) s[h] = 0.f;
-                o[h] = offsets_of(ZEROS ? lds_8(p + kZeroAt + (low & 3) + gi) & 15u : 8u);
-              }
-              float d[NT][4];
-              constexpr int kSteps = 4 / kGroups;
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-              for (int i = gi * kSteps; i < (gi + 1) * kSteps; ++i) {
-                uint32_t p[4], q[4];
-                unpack_word(p, w0[i], o[0]);
-                unpack_word(q, w1[i], o[1]);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  if (i == gi * kSteps) mma_first(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
-                  else mma_next(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
-                  mma_next(d[n], p[2], q[2], p[3], q[3], b[i][n].z, b[i][n].w);
-                }
-              }
+              for (int c = 0; c < 4; ++c) acc[r][n][c] = 0.f;
+#pragma unroll 1
+          for (; c_unit < nunits; c_unit += a.team) {
+            cp_async_wait<kDepth - 2>();
+            __syncwarp();  // every lane's copies are here, and the slot before is free
+            fetch();
+            uint4 b[4][NT];
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[r][n][c] = fmaf(s[c >> 1], d[n][c], acc[r][n][c]);
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t off = c_unit * xstep[n];
+              b[0][n] = lds_128(xe[n] + off);
+              b[1][n] = lds_128(xo[n] + off + 64);
+              b[2][n] = lds_128(xe[n] + off + 128);
+              b[3][n] = lds_128(xo[n] + off + 192);
             }
+            const int group0 = (u0 + c_unit) * kGroups;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              uint32_t w0[4], w1[4];
+              load_words<G>(w0, slot + (r * 16 + g) * kRowBytes, t);
+              load_words<G>(w1, slot + (r * 16 + 8 + g) * kRowBytes, t);
+              const uint32_t sc = slot + kScaleAt + (r * 16 + g) * kScaleStride;
+#pragma unroll
+              for (int gi = 0; gi < kGroups; ++gi) {
+                // Scale and zero point of the two rows' group.
+                float s[2];
+                Offsets o[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t p = sc + h * 8 * kScaleStride;
+                  const int low = el_low[r][h] + group0;
+                  if constexpr (ST == AR_TYPE_F32) {
+                    s[h] = __uint_as_float(lds_32(p + gi * 4));
+                  } else if constexpr (G == 128) {
+                    // The upper or the lower half of the word, as the upper one.
+                    const uint32_t v = __byte_perm(lds_32(p), 0, (low & 1) * 0x2200 + 0x1044);
+                    s[h] = ST == AR_TYPE_BF16
+                               ? __uint_as_float(v)
+                               : __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
+                  } else {
+                    const uint32_t v = lds_16(p + (el_low[r][h] & 1) * 2 + gi * 2);
+                    s[h] = ST == AR_TYPE_BF16
+                               ? __uint_as_float(v << 16)
+                               : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+                  }
+                  // Behind the row's end stands another row's scale.
+                  if (kGroups > 1 && group0 + gi >= a.ng) s[h] = 0.f;
+                  o[h] = offsets_of(ZEROS ? lds_8(p + kZeroAt + (low & 3) + gi) & 15u : 8u);
+                }
+                float d[NT][4];
+                constexpr int kSteps = 4 / kGroups;
+#pragma unroll
+                for (int i = gi * kSteps; i < (gi + 1) * kSteps; ++i) {
+                  uint32_t p[4], q[4];
+                  unpack_word(p, w0[i], o[0]);
+                  unpack_word(q, w1[i], o[1]);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    if (i == gi * kSteps)
+                      mma_first(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
+                    else
+                      mma_next(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
+                    mma_next(d[n], p[2], q[2], p[3], q[3], b[i][n].z, b[i][n].w);
+                  }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) acc[r][n][c] = fmaf(s[c >> 1], d[n][c], acc[r][n][c]);
+              }
+            }
+            slot += kSlot;
+            if (slot == ring + kDepth * kSlot) slot = ring;
           }
-        }
-        c_unit -= units;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[r][n][c] *= up[n][c & 1];
-      }
-
-      if (a.team == 1 && S == 1) {  // the warp has the whole sums
-        if (has) {
-          const int o0 = block * outs + g;
+          c_unit -= nunits;
+          // Back to the columns' powers of two.
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              __nv_bfloat16 *p = op[n][c] + o0;
-              if (op[n][c] == nullptr) continue;
+              const int col = min(it.col + n * 8 + 2 * t + c, kW4MaxXCols - 1);
+              const float up = __int_as_float((127 + exponent_of(col_top[col])) << 23);
 #pragma unroll
-              for (int r = 0; r < R; ++r) {
-                if (act) {
-                  if (o0 + r * 8 < a.width)
-                    p[r * 8] = __float2bfloat16_rn(gated(acc[r][n][c], acc[r][n][c + 2]));
+              for (int r = 0; r < R; ++r) acc[r][n][c] *= up, acc[r][n][c + 2] *= up;
+            }
+
+          if (a.team == 1) {  // the warp has the whole sums of the phase
+            float *sum = sums + (round * teams + team) * tile;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int col = n * 8 + 2 * t + c;
+                if (col >= it.ncols) continue;
+                const int o0 = it.block * outs + g;
+                __nv_bfloat16 *to = a.out + static_cast<int64_t>(col_pair[it.col + col]) * a.width + o0;
+                float v[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float *p = sum + col * kRows + r * 16 + h * 8 + g;
+                    v[r][h] = acc[r][n][c + 2 * h];
+                    if (!first) v[r][h] += *p;
+                    if (!last) *p = v[r][h];
+                  }
+                if (!last) continue;
+                if (act) {  // R = 1: gate and up rows eight apart, R = 2: sixteen
+                  if constexpr (R == 1) {
+                    if (o0 < a.width) to[0] = __float2bfloat16_rn(gated(v[0][0], v[0][1]));
+                  } else {
+                    if (o0 < a.width) to[0] = __float2bfloat16_rn(gated(v[0][0], v[1][0]));
+                    if (o0 + 8 < a.width) to[8] = __float2bfloat16_rn(gated(v[0][1], v[1][1]));
+                  }
                 } else {
-                  if (o0 + r * 16 < a.width) p[r * 16] = __float2bfloat16_rn(acc[r][n][c]);
-                  if (o0 + r * 16 + 8 < a.width) p[r * 16 + 8] = __float2bfloat16_rn(acc[r][n][c + 2]);
+#pragma unroll
+                  for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                      if (o0 + r * 16 + h * 8 < a.width)
+                        to[r * 16 + h * 8] = __float2bfloat16_rn(v[r][h]);
                 }
               }
-            }
-        }
-        continue;
-      }
-      // The warps' sums: red[parity][warp][column][row].  A buffer is written
-      // again two items on, behind a barrier that every reader has passed.
-      const int stride = a.cols * kRows;
-      float *buf = red + (parity * warps + team * a.team) * stride;
-      parity ^= 1;
-      if (has) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int col = n * 8 + 2 * t + (c & 1), row = r * 16 + (c >> 1) * 8 + g;
-              if (col < ncols) buf[member * stride + col * kRows + row] = acc[r][n][c];
-            }
-      }
-      if (S > 1) {
-        __syncwarp();
-        cluster_arrive_release();
-        cluster_wait_acquire();
-      } else if (has) {
-        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(a.team * 32) : "memory");
-      }
-      if (has) {
-        auto sum_of = [&](int col, int row) -> float {
-          float v = 0.f;
-          const float *p = buf + col * kRows + row;
-          if (S == 1) {
-            for (int w = 0; w < a.team; ++w) v += p[w * stride];
-          } else {
-            for (int c = 0; c < S; ++c)
-              for (int w = 0; w < a.team; ++w) v += ld_cluster_f32(p + w * stride, c);
+            continue;
           }
-          return v;
-        };
-        for (int i = (member * 32 + lane) * S + rank; i < ncols * outs; i += a.team * 32 * S) {
-          const int col = i / outs, o = i - col * outs;
-          const int row = act ? (o >> 3) * 16 + (o & 7) : o;
-          float v = sum_of(col, row);
-          if (act) v = gated(v, sum_of(col, row + 8));
-          if (block * outs + o < a.width)
-            a.out[static_cast<int64_t>(col_pair[col]) * a.width + block * outs + o] =
-                __float2bfloat16_rn(v);
+          // The sums go to the team's buffer, which every warp has read since
+          // the item before last; then the item before is added up.
+          const int at2 = team * 2 + (done & 1);
+          if (done >= 2)
+            mbar_wait_bounded(&empty[at2], ((done >> 1) + 1) & 1, &aborted, a.wait_limit_ns, a.status);
+          float *buf = red + (at2 * a.team + member) * tile;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int col = n * 8 + 2 * t + (c & 1), row = r * 16 + (c >> 1) * 8 + g;
+                if (col < it.ncols) buf[col * kRows + row] = acc[r][n][c];
+              }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[at2]);
+          if (pending) gather(left, done - 1, first, last);
+          left = it;
+          pending = true;
+          ++done;
         }
+        if (pending) {  // col_pair is about to change
+          gather(left, done - 1, first, last);
+          pending = false;
+        }
+        at = end;
       }
     }
-    seg = seg_end;
+    base = chunk;
   }
   cp_async_wait<0>();
-  if (S > 1) {  // no CTA leaves while another reads its sums
-    __syncwarp();
-    cluster_arrive_release();
-    cluster_wait_acquire();
-  }
 }
 
 using W4Kernel = void (*)(W4Args);
-template <int ST, bool ZEROS, bool EXPERTS, int R, int NT>
-inline W4Kernel w4_pick_group(int group) {
-  return group == 32 ? &k_w4_matvec<R, NT, 32, ST, ZEROS, EXPERTS>
-         : group == 64 ? &k_w4_matvec<R, NT, 64, ST, ZEROS, EXPERTS>
-                       : &k_w4_matvec<R, NT, 128, ST, ZEROS, EXPERTS>;
-}
+// Row tiles 1 or 2 (1 with groups of 32, whose scales would fill the
+// registers), column tiles 1 or 2.
 template <int ST, bool ZEROS, bool EXPERTS>
-inline W4Kernel w4_pick_tile(int r, int nt, int group) {
-  if (nt == 1)
-    return r == 1 ? w4_pick_group<ST, ZEROS, EXPERTS, 1, 1>(group)
-                  : w4_pick_group<ST, ZEROS, EXPERTS, 2, 1>(group);
-  return r == 1 ? w4_pick_group<ST, ZEROS, EXPERTS, 1, 2>(group)
-                : w4_pick_group<ST, ZEROS, EXPERTS, 2, 2>(group);
+inline W4Kernel w4_pick(int r, int nt, int group) {
+  if (group == 32)
+    return nt == 1 ? &k_w4_matvec<1, 1, 32, ST, ZEROS, EXPERTS>
+                   : &k_w4_matvec<1, 2, 32, ST, ZEROS, EXPERTS>;
+  if (group == 64)
+    return nt == 1 ? (r == 1 ? &k_w4_matvec<1, 1, 64, ST, ZEROS, EXPERTS>
+                             : &k_w4_matvec<2, 1, 64, ST, ZEROS, EXPERTS>)
+                   : (r == 1 ? &k_w4_matvec<1, 2, 64, ST, ZEROS, EXPERTS>
+                             : &k_w4_matvec<2, 2, 64, ST, ZEROS, EXPERTS>);
+  return nt == 1 ? (r == 1 ? &k_w4_matvec<1, 1, 128, ST, ZEROS, EXPERTS>
+                           : &k_w4_matvec<2, 1, 128, ST, ZEROS, EXPERTS>)
+                 : (r == 1 ? &k_w4_matvec<1, 2, 128, ST, ZEROS, EXPERTS>
+                           : &k_w4_matvec<2, 2, 128, ST, ZEROS, EXPERTS>);
 }
 
 }  // namespace arn
