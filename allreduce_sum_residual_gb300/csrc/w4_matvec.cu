@@ -61,12 +61,14 @@ static int allow_shared_memory(int bytes) {
 
 struct W4Plan {
   int r, nt, warps, team, phase_units, cols, x_cols;
-  int64_t sets;  // most column sets
+  int64_t sets;    // most column sets
+  int64_t rounds;  // items of a team, about
 };
 
 // Lays out shared memory for a plan, with as many columns of x as fit into
 // `most` (and no more than sets could fill); false if not even one set does.
-static bool w4_layout(W4Plan *p, int group, int64_t most, bool experts, W4Args *a) {
+// `rounds`: items a team has to walk.
+static bool w4_layout(W4Plan *p, int group, int64_t rounds, int64_t most, bool experts, W4Args *a) {
   const bool phased = p->phase_units < a->units;
   const int64_t column = int64_t{p->phase_units} * 256;
   const int64_t tile = int64_t{p->cols} * 16 * p->r * 4;
@@ -75,6 +77,7 @@ static bool w4_layout(W4Plan *p, int group, int64_t most, bool experts, W4Args *
   const int teams = p->warps / p->team;
   // Sums between phases: as many items a team as 32 KB hold.
   a->phase_rounds = static_cast<int>(32768 / (teams * tile));
+  if (a->phase_rounds > rounds) a->phase_rounds = static_cast<int>(rounds);
   if (a->phase_rounds < 1) a->phase_rounds = 1;
   const int64_t acc = phased ? a->phase_rounds * teams * tile : 0;
   const int64_t ids = experts ? (int64_t{2} * a->pairs + 15) / 16 * 16 : 0;
@@ -97,24 +100,62 @@ static bool w4_layout(W4Plan *p, int group, int64_t most, bool experts, W4Args *
   return true;
 }
 
+// The launch shape: row tiles and team that minimise an estimate of a CTA's
+// time, with the fewest phases whose x fits.
+//   - The CTA with most items goes through them at 27 KB/us with one row tile
+//     (16 x 6144 x 32768 with the activation: 48 us against 50 us with two),
+//     34 KB/us with two and one column tile (32 tokens, 112 experts of 1024 x
+//     6144: 77 us against 97 us): two read x half as often, but leave more to
+//     the last wave (one row, 7168 x 7168: 12.7 us against 11.9 us).
+//   - Warps that find no item idle; twelve busy ones of sixteen reach most of
+//     that rate, eight two thirds of it.
+//   - An item's end costs a team of one 0.2 us, larger teams 0.4 to 1.1 us
+//     (the same 7168 x 7168: 11.9, 13.6 and 14.7 us with teams of 4, 8, 16).
+//   - x takes 0.05 us a KB to unpack and 1.5 us a phase, for every chunk.
 static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
-                    W4Plan *p) {
-  for (p->nt = m <= 8 ? 1 : 2; p->nt >= 1; --p->nt) {
-    p->cols = a->pairs < 8 * p->nt ? a->pairs : 8 * p->nt;
+                    W4Plan *best) {
+  double least = 0;
+  bool found = false;
+  W4Plan p = {};
+  p.warps = kW4MaxWarps;
+  const int per_row = a->act == AR_ACT_SILU_MUL ? 8 : 16;  // outputs of a row tile
+  // Two column tiles where sets of more than eight are the rule.
+  for (p.nt = experts ? (a->pairs > 6 * a->E ? 2 : 1) : (m > 8 ? 2 : 1); p.nt >= 1 && !found;
+       --p.nt) {
+    // A set's columns: at most the batch, whose tokens seldom name an expert
+    // twice (that one then gets two sets).
+    p.cols = static_cast<int>(m < 8 * p.nt ? m : 8 * p.nt);
     // Each set has an expert of its own or is full.
-    p->sets = experts ? a->E + a->pairs / p->cols : (a->pairs + p->cols - 1) / p->cols;
-    if (p->sets > a->pairs) p->sets = a->pairs;
-    for (p->r = group == 32 ? 1 : 2; p->r >= 1; p->r /= 2) {
-      if (p->r > 1 && p->sets * ((a->N + 16 * p->r - 1) / (16 * p->r)) < 4 * sms) continue;
-      p->warps = 16;
-      p->team = a->units >= 48 ? 16 : a->units >= 16 ? 4 : 1;
-      for (int phases = 1; phases <= a->units; ++phases) {
-        p->phase_units = (a->units + phases - 1) / phases;
-        if (w4_layout(p, group, most, experts, a)) return true;
-      }
-    }
+    p.sets = experts ? a->E + a->pairs / p.cols : (a->pairs + p.cols - 1) / p.cols;
+    if (p.sets > a->pairs) p.sets = a->pairs;
+    const int64_t likely = experts && p.sets > a->E ? a->E : p.sets;
+    for (p.r = 1; p.r <= (group == 32 ? 1 : 2); ++p.r)
+      for (p.team = 1; p.team <= p.warps; p.team *= 2)
+        for (int phases = 1; phases <= a->units; ++phases) {
+          p.phase_units = (a->units + phases - 1) / phases;
+          const int64_t items = likely * ((a->width + per_row * p.r - 1) / (per_row * p.r));
+          const int64_t each = (items + sms - 1) / sms;
+          const int teams = p.warps / p.team;
+          p.rounds = (each + teams - 1) / teams;
+          if (!w4_layout(&p, group, p.rounds, most, experts, a)) continue;
+          const double n = static_cast<double>(each), rounds = static_cast<double>(p.rounds);
+          const double busy = p.warps * n / (rounds * teams);
+          double rate = p.r == 1 ? 27 : p.nt == 1 ? 34 : 30;
+          if (busy < 12) rate *= busy < 8 ? busy / 12 : 0.67 + (busy - 8) / 12;
+          const double chunks = phases == 1 ? 1 : (rounds + a->phase_rounds - 1) / a->phase_rounds;
+          const double time = n * p.r * a->units / rate +
+                              rounds * phases * (p.team == 1 ? 0.2 : 0.3 + 0.05 * p.team) +
+                              chunks * (0.05 * p.cols * a->K / 512 + 1.5 * phases);
+          if (!found || time < least) {
+            least = time;
+            *best = p;
+            found = true;
+          }
+          break;
+        }
   }
-  return false;
+  if (found) w4_layout(best, group, best->rounds, most, experts, a);
+  return found;
 }
 
 static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k, const void *q,

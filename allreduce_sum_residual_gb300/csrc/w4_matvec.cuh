@@ -254,6 +254,14 @@ __device__ __forceinline__ int w4_row(const W4Args &a, int block, int lr) {
   return min(block * 16 * R + lr, a.N - 1);
 }
 
+// This CTA's share of `total` items (at most 4096 sets x 65536 blocks).
+__device__ __forceinline__ void w4_range(int total, int *first, int *end) {
+  const unsigned each = static_cast<unsigned>(total) / gridDim.x;
+  const unsigned more = static_cast<unsigned>(total) - each * gridDim.x;
+  *first = static_cast<int>(blockIdx.x * each + min(blockIdx.x, more));
+  *end = *first + static_cast<int>(each + (blockIdx.x < more ? 1u : 0u));
+}
+
 // A warp's way through its CTA's items [item0, item1): chunk by chunk, in
 // each chunk phase by phase, in each phase the team's items, and of all their
 // units in a row every team'th.  One phase: one chunk.
@@ -358,10 +366,11 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   if constexpr (!EXPERTS) {
     // The first units' lines on their way to L2 while the previous grid
     // drains: nothing enters this SM before the wait.
-    const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
-    const int64_t item = total * blockIdx.x / gridDim.x + team;
-    if (item < total * (blockIdx.x + 1) / gridDim.x && (t & 1) == 0) {
-      const int block = static_cast<int>(item % a.row_blocks);
+    int item, end;
+    w4_range(nsets * a.row_blocks, &item, &end);
+    item += team;
+    if (item < end && (t & 1) == 0) {
+      const int block = item % a.row_blocks;
       const int64_t row_bytes = a.K / 2;
       for (int d = 0, u = member; d < kDepth - 1 && u < a.phase_units; ++d, u += a.team) {
         const int64_t piece = static_cast<int64_t>(u) * 64 + t * 16;
@@ -426,9 +435,8 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   } else {
     __syncthreads();  // the barriers are there
   }
-  const int64_t total = static_cast<int64_t>(nsets) * a.row_blocks;
-  const int item0 = static_cast<int>(total * blockIdx.x / gridDim.x);
-  const int item1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  int item0, item1;
+  w4_range(nsets * a.row_blocks, &item0, &item1);
 
   // The expert of a column set.
   auto expert_of = [&](int set) -> int {
@@ -533,47 +541,62 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
 
   // Units [u0, u1) of the first n columns into shared memory, as fp16 times
   // their powers of two: [unit][column][step][lane], odd columns with the
-  // steps of a pair exchanged (no bank conflicts between two columns).
+  // steps of a pair exchanged (no bank conflicts between two columns).  A
+  // column's eights go to one warp, or to as many as there are for it; eight
+  // loads of a lane are under way at a time.
   auto stage = [&](int u0, int u1, int n) {
     const int pieces = (u1 - u0) * 16;  // eights of a column
-    auto place = [&](int i, int *col) -> uint4 * {  // of eight i of all columns
-      *col = i / pieces;
-      const int j = i - *col * pieces, to = step_lane<G>(j & 15);
-      return xs + ((j >> 4) * a.x_cols + *col) * 16 + (to ^ ((*col & 1) << 2));
+    const int share = n < warps ? warps / n : 1;  // warps of a column
+    const int step = share * 32, j0 = warp % share * 32 + lane;
+    auto place = [&](int j, int col) -> uint4 * {
+      const int to = step_lane<G>(j & 15);
+      return xs + ((j >> 4) * a.x_cols + col) * 16 + (to ^ ((col & 1) << 2));
     };
-    for (int i0 = 0; i0 < pieces * n; i0 += threads) {
-      // Sixteen lanes hold eights of one column.
-      const int i = i0 + tid;
-      int col, top = 0;
-      uint4 *to = place(i, &col);
-      if (col < n) {
-        const int at = u0 * 16 + i - col * pieces;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (at * 8 < a.K)
-          w = __ldg(a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + at);
-        float f[8];
-        unpack8(w, f);
+    for (int col = warp / share; col < n; col += warps / share) {
+      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8);
+      int top = 0;
+      for (int j = j0; j < pieces; j += 8 * step) {
+        uint4 w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int bits = __float_as_int(f[e]) & 0x7FFFFFFF;
-          if (bits < 0x7F800000 && bits > top) top = bits;
+        for (int i = 0; i < 8; ++i) {
+          const int at = j + i * step;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (at < pieces && (u0 * 16 + at) * 8 < a.K) w[i] = __ldg(row + u0 * 16 + at);
         }
-        *to = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632),
-                         __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
-      }
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      if ((lane & 15) == 0 && col < n && top > 0) atomicMax(&col_top[col], top);
+        for (int i = 0; i < 8; ++i) {
+          const int at = j + i * step;
+          if (at >= pieces) break;
+          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // the upper 16 bits of an fp32 are a bf16
+            const int lo = v[e] << 16 & 0x7FFF0000, hi = v[e] & 0x7FFF0000;
+            top = max(top, lo < 0x7F800000 ? lo : 0);
+            top = max(top, hi < 0x7F800000 ? hi : 0);
+          }
+          *place(at, col) =
+              make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                         __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+        }
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) {
+        if (share == 1) col_top[col] = top;
+        else atomicMax(&col_top[col], top);
+      }
     }
-    __syncthreads();
-    for (int i = tid; i < pieces * n; i += threads) {  // what this thread has put there
-      int col;
-      uint4 *to = place(i, &col);
+    if (share > 1) __syncthreads();
+    else __syncwarp();
+    for (int col = warp / share; col < n; col += warps / share) {
       const float down = __int_as_float((127 - exponent_of(col_top[col])) << 23);
-      uint4 v = *to;
-      v.x = halves_of(v.x, down), v.y = halves_of(v.y, down);
-      v.z = halves_of(v.z, down), v.w = halves_of(v.w, down);
-      *to = v;
+#pragma unroll 4
+      for (int j = j0; j < pieces; j += step) {  // what this lane has put there
+        uint4 *to = place(j, col);
+        uint4 v = *to;
+        v.x = halves_of(v.x, down), v.y = halves_of(v.y, down);
+        v.z = halves_of(v.z, down), v.w = halves_of(v.w, down);
+        *to = v;
+      }
     }
     __syncthreads();
   };
@@ -627,7 +650,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       for (int at = base; at < chunk;) {
         // The column sets from item `at` on that fit together: [at, end).
         const int set0 = at / a.row_blocks;
-        __syncthreads();  // nobody uses the sets before any more
+        if (at != item0 || u0 != 0) __syncthreads();  // nobody uses the sets before any more
         if (warp == 0) {
           const int set = set0 + lane;
           const bool there = set < nsets && set * a.row_blocks < chunk;
@@ -651,13 +674,16 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
           }
           if (fit >> lane & 1u) set_col[lane + 1] = before;
         }
-        for (int c = tid; c < kW4MaxXCols; c += threads) col_top[c] = 0;
+        for (int c = tid; c < kW4MaxXCols; c += threads) {
+          col_top[c] = 0;
+          if constexpr (!EXPERTS) col_pair[c] = set0 * a.cols + c;  // the sets are full but the last
+        }
         __syncthreads();
         const int count = set_count;
         const int end = min(chunk, (set0 + count) * a.row_blocks);
-        for (int i = warp; i < count; i += warps) {  // the sets' pairs, in order
-          const int c0 = set_col[i], n = set_col[i + 1] - c0;
-          if constexpr (EXPERTS) {
+        if constexpr (EXPERTS) {
+          for (int i = warp; i < count; i += warps) {  // the sets' pairs, in order
+            const int c0 = set_col[i], n = set_col[i + 1] - c0;
             const int e = set_expert[i], skip = (set0 + i - sets[e]) * a.cols;
             int seen = 0;
             for (int p0 = 0; p0 < a.pairs && seen < skip + n; p0 += 32) {
@@ -667,11 +693,9 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
               if (is && k >= 0 && k < n) col_pair[c0 + k] = p0 + lane;
               seen += __popc(who);
             }
-          } else {
-            if (lane < n) col_pair[c0 + lane] = (set0 + i) * a.cols + lane;
           }
+          __syncthreads();
         }
-        __syncthreads();
         stage(u0, u1, set_col[count]);
 
 #pragma unroll 1
