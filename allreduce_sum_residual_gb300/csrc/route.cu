@@ -2,20 +2,28 @@
 //
 // One warp takes one token.  A group of experts lies on L = 32 / 2^ceil(log2
 // groups) neighbouring lanes, V = ceil(group size / L) neighbouring experts
-// on each, so that (lane, register) order is expert order: "lowest index of
-// the largest" is the lowest lane of a ballot, then its lowest register.
-// A group's score is a butterfly over its L lanes.  The k rounds of the
-// top-k are one integer max over the warp (redux) and one ballot each, on
-// keys that order like the choices.
+// on each.  A group's score is a butterfly over its L lanes.
 //
-// Equal to 64 bits.  A choice computed in fp32 is off by a few 2^-24, so two
-// experts that close can come out in the wrong order, and with 256 experts
-// that happens about once in a thousand rows.  The kernel therefore also
-// finds the (k+1)-th choice, and a row in which two neighbours of that order
-// (or the last kept and the first dropped group) are nearer than the error
-// bound is done again in fp64 by its warp.  Neighbours with the same logit
-// and bias are exact ties, which need no second look, and so does nothing
-// where the choices rank as the logits: those are compared as they are.
+// Top-k.  Every choice becomes a 32-bit key, its order in the upper 23 bits
+// and 511 - expert in the lower nine, so that keys are distinct and equal
+// choices order by index.  A lane sorts its V keys (a merge network of max
+// and min); a round is then one integer max over the warp (redux), which
+// names the expert, and the lane that held it moves up its next key.
+//
+// Equal to 64 bits.  23 bits, and fp32 scores off by a few 2^-24, can put two
+// experts in the wrong order.  The kernel therefore also finds the (k+1)-th
+// choice and looks at neighbours of that order that are nearer than the error
+// bound.  Where they are all that is near (a few rows in a thousand), the k +
+// 1 sigmoids are computed again in fp64, one a lane, and sorted by those;
+// otherwise (another expert near the last choice; a group border too near to
+// call; softmax scores) the warp does the whole row again, in fp64, or in
+// fp32 where the choices rank as the logits and those are compared as they
+// are.  Neighbours with the same logit and bias are exact ties, which need no
+// second look.
+//
+// Bound by instructions, some 450 a row of 256 experts: 16384 such rows with
+// groups and bias take 12 us (52 us with k passes over every lane's choices
+// in place of the keys), where their bytes would take 2.6 us.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -129,13 +137,12 @@ __device__ __forceinline__ F choice_of(const RouteArgs &a, float x, float bias, 
   return c > F(-INFINITY) ? c : F(-INFINITY);
 }
 
-// The order of a row: lane j <= k returns the id of its (j+1)-th choice (-1
-// where there are fewer candidates).  *close: whether the group border is
-// nearer than the error of two group scores, 2 delta; the caller looks at
-// the rest.  x: this lane's logits, of which those in `valid` exist.
+// The order of a row, choice by choice in F: lane j <= k returns the id of its
+// (j+1)-th choice (-1 where there are fewer candidates).  x: this lane's
+// logits, of which those in `valid` exist.
 template <typename F, int V>
 __device__ __forceinline__ int order_row(const RouteArgs &a, const float (&x)[V], uint32_t valid,
-                                         int first, const Scale<F> &sc, F delta, bool *close) {
+                                         int first, const Scale<F> &sc) {
   using K = typename Key<F>::type;
   constexpr K kOut = Key<F>::kOut, kDead = kOut + 1;
   const int lane = threadIdx.x & 31;
@@ -156,7 +163,6 @@ __device__ __forceinline__ int order_row(const RouteArgs &a, const float (&x)[V]
       }
     }
   }
-  *close = false;
   if (a.topk_groups < a.groups) {
     for (int o = 1; o < 1 << a.lanes_log2; o <<= 1) {
       const F h = __shfl_xor_sync(0xFFFFFFFFu, hi, o), s = __shfl_xor_sync(0xFFFFFFFFu, second, o);
@@ -172,15 +178,6 @@ __device__ __forceinline__ int order_row(const RouteArgs &a, const float (&x)[V]
       rank += g != group && (other > mine || (other == mine && g < group)) ? 1 : 0;
     }
     const bool kept = rank < a.topk_groups;
-    F above = F(INFINITY), below = F(-INFINITY);  // border: the worst kept, the best dropped
-    for (int g = 0; g < a.groups; ++g) {
-      const F other = __shfl_sync(0xFFFFFFFFu, mine, g << a.lanes_log2);
-      const bool in = __shfl_sync(0xFFFFFFFFu, kept ? 1 : 0, g << a.lanes_log2) != 0;
-      if (in) above = other < above ? other : above;
-      else below = other > below ? other : below;
-    }
-    // Dropped groups at -inf are below every number, and -inf equals -inf.
-    *close = below > F(-INFINITY) && !(above - below > delta + delta);
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (!kept) key[i] = kOut;
@@ -211,18 +208,53 @@ __device__ __forceinline__ int order_row(const RouteArgs &a, const float (&x)[V]
   return id;
 }
 
-// The same row in fp64, out of the way of the common path's registers.
+// Out of the way of the common path's registers.
 template <int V>
-__device__ __noinline__ int order_row_64(const RouteArgs &a, const float (&x)[V], uint32_t valid,
-                                         int first) {
-  bool close;
+__device__ __noinline__ int order_row_exactly(const RouteArgs &a, const float (&x)[V],
+                                              uint32_t valid, int first) {
+  if (a.by_logit) return order_row<float, V>(a, x, valid, first, Scale<float>{0.f, 1.f});
   Scale<double> s{0.0, 1.0};
   if (a.softmax) s = scale_of<double, V>(x);
-  return order_row<double, V>(a, x, valid, first, s, 0.0, &close);
+  return order_row<double, V>(a, x, valid, first, s);
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const __grid_constant__ RouteArgs a) {
+// A score to a few 2^-24 of 1, in few instructions: ex2.approx is off by 2
+// ulp and its argument by half of one (of x - top or x, whose exponential or
+// derivative makes up for its size), rcp.approx by 1.
+__device__ __forceinline__ float quick_score(const RouteArgs &a, float x, float top, float inv) {
+  if (a.softmax) return __expf(x - top) * inv;
+  return __fdividef(1.f, 1.f + __expf(-x));
+}
+
+// A logit's order in the upper 23 bits, 2 or more; whole if it has 16.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t logit_order(float x) {
+  const uint32_t order = static_cast<uint32_t>(order_key(x)) ^ 0x80000000u;
+  return (EXACT ? order >> 4 : order) & ~511u;  // a half widens to 19 bits
+}
+
+// Sorts descending (Batcher's odd-even merges; V a power of two).
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+          if (i + j + d < V && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
+            const uint32_t lo = min(k[i + j], k[i + j + d]), hi = max(k[i + j], k[i + j + d]);
+            k[i + j] = hi;
+            k[i + j + d] = lo;
+          }
+}
+
+// LOGIT: a.by_logit.  Registers for eight CTAs an SM (four, two): the common
+// path fits, the second look spills.
+template <typename T, int V, bool LOGIT>
+__global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2) k_route(const __grid_constant__ RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int group = lane >> a.lanes_log2;
   const int in_group = (lane & ((1 << a.lanes_log2) - 1)) * V;
@@ -234,6 +266,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const __grid_constan
   const uint32_t valid = count >= 32 ? 0xFFFFFFFFu : (1u << count) - 1u;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+  // The bias, and the range [-reach, 1 + reach] of the finite choices.
+  float bias[V], reach = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bias[i] = a.bias != nullptr && i < count ? __ldg(a.bias + first + i) : 0.f;
+    const float b = fabsf(bias[i]);
+    if (b < INFINITY) reach = fmaxf(reach, b);  // an infinite choice is exact
+  }
+  if (a.bias != nullptr) reach = warp_max(reach);
+  // Keys in fixed point: `fine` steps in 1, from 3 (for -reach) on; a sum of
+  // two choices in half the steps.
+  const float fine = 8388590.f / (1.f + 2.f * reach), base = fmaf(reach, fine, 3.f);
+  // How near two fp32 choices can be to come out in the wrong order.  In
+  // 2^-24 of 1 + reach: a quick sigmoid is off by 6 at most, a softmax score
+  // by 6 and its row's sum of up to 37 rounded adds, the sum with the bias by
+  // 1, the key by 1.5 steps of 4: twice that is under 2^-19 and 2^-16.
+  const float delta = (1.f + reach) * (a.softmax ? 0x1p-16f : 0x1p-19f);
+  constexpr bool kExact = sizeof(T) == 2;  // keys that hold a logit whole
+
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); row < a.m;
        row += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
     const T *p = static_cast<const T *>(a.x) + row * a.stride;
@@ -262,38 +313,151 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const __grid_constan
     // Softmax needs the row's sum only for scores: not for choices that rank
     // as the logits, nor for weights that are renormalised.
     Scale<float> sc{0.f, 1.f};
-    if (a.softmax && !(a.by_logit && a.renorm)) sc = scale_of<float, V>(x);
-    // Error bound of the difference of two fp32 choices, in 2^-24 of the
-    // largest choice.  A sigmoid (exp within 1 ulp, an add, a divide) is off
-    // by 4, a softmax score by 4 and its row's sum of up to 37 rounded adds,
-    // the sum with the bias by 1; twice that is under 2^-20 and 2^-17.
-    float delta = 0.f;
-    if (!a.by_logit) {
-      float big = 1.f;
-      if (a.bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i < count) {
-            const float b = fabsf(__ldg(a.bias + first + i));
-            if (b < INFINITY) big = fmaxf(big, 1.f + b);  // an infinite choice is exact
-          }
-        big = warp_max(big);
-      }
-      delta = big * (a.softmax ? 0x1p-17f : 0x1p-20f);
+    float inv = 1.f;
+    if (a.softmax && !(LOGIT && a.renorm)) {
+      sc = scale_of<float, V>(x);
+      inv = 1.f / sc.sum;
     }
-    bool close;
-    int id = order_row<float, V>(a, x, valid, first, sc, delta, &close);
+    // Choices (-inf: off) and keys.  0: no candidate; 1 in the upper bits:
+    // off; from 2 on the choices, as fixed point, or the logits' own order.
+    float c[V];
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      uint32_t order;
+      if constexpr (LOGIT) {
+        c[i] = x[i];
+        order = logit_order<kExact>(x[i]);
+      } else {
+        c[i] = quick_score(a, x[i], sc.top, inv) + bias[i];
+        order = static_cast<uint32_t>(fminf(fmaf(c[i], fine, base), 8388600.f)) << 9;  // 2 or more
+      }
+      if (!(x[i] > -INFINITY) || !(c[i] > -INFINITY)) {
+        c[i] = -INFINITY;
+        order = 1u << 9;
+      }
+      key[i] = i < count ? order | static_cast<uint32_t>(511 - first - i) : 0u;
+    }
+    bool close = false;
+    bool kept = true;
+    if (a.topk_groups < a.groups) {
+      float hi = -INFINITY, second = -INFINITY;  // the two largest choices
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float v = i < count ? c[i] : -INFINITY;
+        second = fmaxf(second, fminf(hi, v));
+        hi = fmaxf(hi, v);
+      }
+      for (int o = 1; o < 1 << a.lanes_log2; o <<= 1) {
+        const float h = __shfl_xor_sync(0xFFFFFFFFu, hi, o);
+        const float s = __shfl_xor_sync(0xFFFFFFFFu, second, o);
+        second = fmaxf(fminf(hi, h), fmaxf(second, s));
+        hi = fmaxf(hi, h);
+      }
+      // -inf with too few experts that are on
+      const float mine = !a.top2 ? hi : second > -INFINITY ? hi + second : -INFINITY;
+      // The groups' keys, and as many rounds as groups are kept.
+      uint32_t order = 1u << 9;
+      if (mine > -INFINITY)
+        order = LOGIT ? logit_order<kExact>(mine)
+                      : static_cast<uint32_t>(fminf(fmaf(mine, 0.5f * fine, base), 8388600.f)) << 9;
+      uint32_t score = group < a.groups ? order | static_cast<uint32_t>(511 - group) : 0u;
+      kept = false;
+      uint32_t best = 0u;
+      for (int r = 0; r < a.topk_groups; ++r) {
+        best = __reduce_max_sync(0xFFFFFFFFu, score);
+        if (score == best) {
+          kept = true;
+          score = 0u;
+        }
+      }
+      kept = kept && group < a.groups;
+      // The border: the worst kept, the best dropped.  Dropped groups at -inf
+      // are below every number, and -inf equals -inf.
+      const uint32_t next = __reduce_max_sync(0xFFFFFFFFu, score);
+      if (next >> 9 > 1u) {
+        if constexpr (LOGIT) {
+          close = !kExact && best >> 9 == next >> 9;
+        } else {
+          const int last_lane = (511 - static_cast<int>(best & 511u)) << a.lanes_log2;
+          const int next_lane = (511 - static_cast<int>(next & 511u)) << a.lanes_log2;
+          const float above = __shfl_sync(0xFFFFFFFFu, mine, last_lane);
+          const float below = __shfl_sync(0xFFFFFFFFu, mine, next_lane);
+          close = !(above - below > delta + delta);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (!kept) key[i] = 0u;
+    }
+    sort_keys<V>(key);
+    uint32_t mine = 0u;  // lane j: the (j+1)-th key
+    for (int r = 0; r <= a.k; ++r) {
+      const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+      if (lane == r) mine = best;
+      if (key[0] == best) {  // one lane, or none left anywhere
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0u;
+      }
+    }
+    int id = mine != 0u ? 511 - static_cast<int>(mine & 511u) : -1;
     float xs = id >= 0 ? to_float(p[id]) : -INFINITY;
-    if (!a.by_logit) {
+    {
       const float bs = id >= 0 && a.bias != nullptr ? __ldg(a.bias + id) : 0.f;
-      const float c = id >= 0 ? choice_of<float>(a, xs, bs, sc) : -INFINITY;
-      const float cn = __shfl_down_sync(0xFFFFFFFFu, c, 1);
+      const uint32_t order = mine >> 9;
+      const float cs = order > 1u ? (LOGIT ? xs : quick_score(a, xs, sc.top, inv) + bs) : -INFINITY;
+      const uint32_t on = __shfl_down_sync(0xFFFFFFFFu, order, 1);
+      const float cn = __shfl_down_sync(0xFFFFFFFFu, cs, 1);
       const float xn = __shfl_down_sync(0xFFFFFFFFu, xs, 1);
       const float bn = __shfl_down_sync(0xFFFFFFFFu, bs, 1);
-      const bool near = lane < a.k && cn > -INFINITY && !(c - cn > delta) &&
-                        !(xs == xn && bs == bn);
-      if (__any_sync(0xFFFFFFFFu, near || close)) {
-        id = order_row_64<V>(a, x, valid, first);
+      const bool same = xs == xn && bs == bn;
+      const bool chosen = lane < a.k && on > 1u;  // experts that are off stand in their order
+      bool again = close;
+      if constexpr (LOGIT) {
+        if (!kExact)
+          again |= __any_sync(0xFFFFFFFFu, chosen && order == on && (!same || lane == a.k - 1));
+      } else {
+        const bool near = __any_sync(0xFFFFFFFFu, chosen && !(cs - cn > delta) && !same);
+        const bool tie = __shfl_sync(0xFFFFFFFFu, chosen && same ? 1 : 0, a.k - 1) != 0;
+        if (near || tie) {
+          // Experts that could belong before the k-th, apart from its equals.
+          const float ck = __shfl_sync(0xFFFFFFFFu, cs, a.k - 1);
+          const float xk = __shfl_sync(0xFFFFFFFFu, xs, a.k - 1);
+          const float bk = __shfl_sync(0xFFFFFFFFu, bs, a.k - 1);
+          int rivals = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            rivals += kept && i < count && !(c[i] <= ck - delta) && c[i] > -INFINITY &&
+                              !(x[i] == xk && bias[i] == bk)
+                          ? 1 : 0;
+          const uint32_t found = __ballot_sync(
+              0xFFFFFFFFu, lane <= a.k && order > 1u && !(cs <= ck - delta) && !(xs == xk && bs == bk));
+          again |= a.softmax || static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rivals)) > __popc(found);
+          if (near && !again) {
+            // These k + 1 in the order of their fp64 choices.
+            double exact = -INFINITY;
+            if (order > 1u) exact = score_of<double>(a, xs, Scale<double>{0.0, 1.0}) + bs;
+            int rank = 0;
+            for (int r = 0; r <= a.k; ++r) {
+              const double other = __shfl_sync(0xFFFFFFFFu, exact, r);
+              const int oid = __shfl_sync(0xFFFFFFFFu, id, r);
+              rank += oid >= 0 && (id < 0 || other > exact || (other == exact && oid < id)) ? 1 : 0;
+            }
+            const int was = id;
+            const float x_was = xs;
+            for (int r = 0; r <= a.k; ++r) {
+              const uint32_t who = __ballot_sync(0xFFFFFFFFu, lane <= a.k && was >= 0 && rank == r);
+              const int src = who ? __ffs(who) - 1 : 0;
+              const int i = __shfl_sync(0xFFFFFFFFu, was, src);
+              const float v = __shfl_sync(0xFFFFFFFFu, x_was, src);
+              if (lane == r) id = who ? i : -1, xs = v;
+            }
+          }
+        }
+      }
+      if (again) {  // the same in every lane
+        id = order_row_exactly<V>(a, x, valid, first);
         xs = id >= 0 ? to_float(p[id]) : -INFINITY;
       }
     }
@@ -323,16 +487,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const __grid_constan
 
 using RouteKernel = void (*)(RouteArgs);
 
-template <typename T>
-static RouteKernel route_kernel(int v) {
+template <typename T, bool LOGIT>
+static RouteKernel route_kernel_of(int v) {
   switch (v) {
-    case 1: return &k_route<T, 1>;
-    case 2: return &k_route<T, 2>;
-    case 4: return &k_route<T, 4>;
-    case 8: return &k_route<T, 8>;
-    case 16: return &k_route<T, 16>;
-    default: return &k_route<T, 32>;
+    case 1: return &k_route<T, 1, LOGIT>;
+    case 2: return &k_route<T, 2, LOGIT>;
+    case 4: return &k_route<T, 4, LOGIT>;
+    case 8: return &k_route<T, 8, LOGIT>;
+    case 16: return &k_route<T, 16, LOGIT>;
+    default: return &k_route<T, 32, LOGIT>;
   }
+}
+template <typename T>
+static RouteKernel route_kernel(int v, bool by_logit) {
+  return by_logit ? route_kernel_of<T, true>(v) : route_kernel_of<T, false>(v);
 }
 
 }  // namespace arn
@@ -397,11 +565,11 @@ extern "C" int ar_route_experts(const void *logits, int logits_type, int64_t row
   a.vec = gs % v == 0 && row_stride * size % vector == 0 && aligned_to(logits, vector);
   a.scale = scale;
   a.status = d->status;
-  RouteKernel kern = logits_type == AR_TYPE_F32 ? route_kernel<float>(v)
-                     : logits_type == AR_TYPE_BF16 ? route_kernel<__nv_bfloat16>(v)
-                                                   : route_kernel<__half>(v);
+  RouteKernel kern = logits_type == AR_TYPE_F32 ? route_kernel<float>(v, a.by_logit)
+                     : logits_type == AR_TYPE_BF16 ? route_kernel<__nv_bfloat16>(v, a.by_logit)
+                                                   : route_kernel<__half>(v, a.by_logit);
   int64_t grid = (m + kRouteWarps - 1) / kRouteWarps;
-  const int64_t cap = static_cast<int64_t>(d->sms) * 16;
+  const int64_t cap = static_cast<int64_t>(d->sms) * 8;  // the bias is read once a warp
   if (grid > cap) grid = cap;
   return launch_pdl(kern, a, grid, kRouteWarps * 32, 0, 1, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
