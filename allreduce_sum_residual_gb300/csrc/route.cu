@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
       }
       key[i] = i < count ? order | static_cast<uint32_t>(511 - first - i) : 0u;
     }
+    sort_keys<V>(key);
     bool close = false;
     bool kept = true;
     if (a.topk_groups < a.groups) {
@@ -386,11 +387,51 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
           close = !(above - below > delta + delta);
         }
       }
+      if (!LOGIT && close && !a.softmax) {  // the same in every lane
+        // The border again in fp64: the groups' three largest keys, and the
+        // two of group j computed by lane j.
+        uint32_t k1 = key[0], k2 = V > 1 ? key[1] : 0u, k3 = V > 2 ? key[2] : 0u;
+        for (int o = 1; o < 1 << a.lanes_log2; o <<= 1) {
+          const uint32_t q1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o);
+          const uint32_t q2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
+          const uint32_t q3 = __shfl_xor_sync(0xFFFFFFFFu, k3, o);
+          const uint32_t lo = min(k1, q1), hi2 = max(k2, q2);  // k1 >= k2 >= k3, the same for q
+          k3 = max(max(k3, q3), min(lo, hi2));
+          k3 = max(k3, min(k2, q2));
+          k2 = max(lo, hi2);
+          k1 = max(k1, q1);
+        }
+        const int leader = lane < a.groups ? lane << a.lanes_log2 : 0;
+        const uint32_t g1 = __shfl_sync(0xFFFFFFFFu, k1, leader);
+        const uint32_t g2 = __shfl_sync(0xFFFFFFFFu, k2, leader);
+        const uint32_t g3 = __shfl_sync(0xFFFFFFFFu, k3, leader);
+        auto exactly = [&](uint32_t of) -> double {
+          if (of >> 9 <= 1u) return -INFINITY;
+          const int e = 511 - static_cast<int>(of & 511u);
+          return score_of<double>(a, to_float(p[e]), Scale<double>{0.0, 1.0}) +
+                 (a.bias != nullptr ? __ldg(a.bias + e) : 0.f);
+        };
+        double sum = exactly(g1);
+        if (a.top2) sum += exactly(g2);  // -inf with too few experts that are on
+        // Whether the next in the group could be one of these after all.
+        const uint32_t in = a.top2 ? g2 : g1, out = a.top2 ? g3 : g2;
+        const bool unsure = lane < a.groups && (sum != sum || (out >> 9 > 1u &&
+                            static_cast<float>((in >> 9) - (out >> 9)) <= delta * fine + 2.f));
+        if (!__any_sync(0xFFFFFFFFu, unsure)) {
+          int rank = 0;
+          for (int g = 0; g < a.groups; ++g) {
+            const double other = __shfl_sync(0xFFFFFFFFu, sum, g);
+            rank += other > sum || (other == sum && g < lane) ? 1 : 0;
+          }
+          const uint32_t in_set = __ballot_sync(0xFFFFFFFFu, lane < a.groups && rank < a.topk_groups);
+          kept = group < a.groups && (in_set >> group & 1u);
+          close = false;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (!kept) key[i] = 0u;
     }
-    sort_keys<V>(key);
     uint32_t mine = 0u;  // lane j: the (j+1)-th key
     for (int r = 0; r <= a.k; ++r) {
       const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key[0]);

@@ -146,6 +146,25 @@ def test_route_many_rows_agree_with_64_bits():
     assert torch.equal(ids, want)
 
 
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_route_decides_near_group_borders_as_64_bits_do(group_score):
+    """Groups whose scores differ by less than fp32 resolves, in every row:
+    eight groups hold the same choices up to a few 2^-25, in another order."""
+    g = gen(14)
+    m, per = 200, 32
+    x = normal(g, 1, per, std=1.0, dtype=torch.float32).repeat(m, 8)
+    x = x.view(m, 8, per)
+    for j in range(8):
+        x[:, j] = x[:, j, torch.randperm(per, generator=g, device=DEV)]
+    s = torch.sigmoid(x.double())
+    s = s + (torch.rand(s.shape, generator=g, device=DEV).double() - 0.5) * 2.0 ** -23
+    x = torch.log(s / (1 - s)).float().reshape(m, 8 * per)
+    b = torch.full((8 * per,), 0.5, device=DEV)
+    kw = dict(bias=b, scoring="sigmoid", groups=8, topk_groups=4, group_score=group_score)
+    w, ids = arn.ar_route_experts(x, 8, **kw)
+    check_route(x, 8, w, ids, **kw)
+
+
 def test_route_nan_and_infinite_values_keep_ids_valid():
     g = gen(6)
     x = normal(g, 32, 64, dtype=torch.float32)
