@@ -21,7 +21,7 @@ Names follow the C ABI:
     ar_get_plan(n, m, H, mode, sm_count=0), ar_get_plan_ex(n, m, H, mode, sm_count, ctas_per_sm),
     ar_route_experts(logits, k, bias=None, ...) -> (weights, ids)
     ar_w4_matvec(x, q, scales, zeros=None, act="none") -> out
-    ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none") -> out
+    ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", first=0) -> out
     ar_combine(y, weights, shared=None, slots=None) -> out
     ar_combine_rmsnorm(y, weights, residual, weight, eps, shared=None, slots=None)
         -> (out, residual_out)
@@ -139,8 +139,8 @@ _SIGS = {
     "ar_w4_matvec": (ctypes.c_int, [_VP, _VP, _VP, ctypes.c_int, _VP, _I64, _I64, _I64,
                                     ctypes.c_int, ctypes.c_int, _VP, _VP]),
     "ar_w4_matvec_experts": (ctypes.c_int, [_VP, ctypes.c_int, _VP, _I64, ctypes.c_int, _VP, _VP,
-                                            ctypes.c_int, _VP, ctypes.c_int, _I64, _I64,
-                                            ctypes.c_int, ctypes.c_int, _VP, _VP]),
+                                            ctypes.c_int, _VP, ctypes.c_int, ctypes.c_int, _I64,
+                                            _I64, ctypes.c_int, ctypes.c_int, _VP, _VP]),
     "ar_combine": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _I64, ctypes.c_int, _I64, _VP, _VP]),
     "ar_combine_rmsnorm": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_float, _I64,
                                           ctypes.c_int, _I64, _VP, _VP, _VP]),

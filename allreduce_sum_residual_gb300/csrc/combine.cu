@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_combine(const __grid_constant
   // Checking build: the row, its pack range, and threads for all of it.
   const bool live = in_bounds(row < a.m && c0 >= 0 && (c1 <= c0 || c1 - c0 <= T) &&
                                   a.k >= 1 && a.k <= AR_MAX_TOPK &&
-                                  S <= static_cast<uint32_t>(kMaxClusterCtas) && q < S,
+                                  (!CL || S <= static_cast<uint32_t>(kMaxClusterCtas)) && q < S,
                               a.status);
   if constexpr (CL) {
     if (threadIdx.x == 0) {

@@ -159,10 +159,10 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
 }
 
 static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k, const void *q,
-                  const void *scales, int scales_type, const void *zeros, int E, int64_t N, int64_t K,
-                  int group, int act, void *out, bool experts, void *stream) {
+                  const void *scales, int scales_type, const void *zeros, int first, int E, int64_t N,
+                  int64_t K, int group, int act, void *out, bool experts, void *stream) {
   const int size = type_size(scales_type);
-  if (m < 0 || k < 1 || E < 1 || N < 1 || K < 1 || size == 0 ||
+  if (m < 0 || k < 1 || first < 0 || E < 1 || N < 1 || K < 1 || size == 0 ||
       (group != 32 && group != 64 && group != 128) || (act != AR_ACT_NONE && act != AR_ACT_SILU_MUL) ||
       (x_per_pair != 0 && x_per_pair != 1))
     return AR_ERR_ARG;
@@ -199,6 +199,7 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.pairs = static_cast<int>(pairs);
   a.k = x_per_pair ? 1 : k;
+  a.first = first;
   a.E = E;
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
@@ -237,15 +238,16 @@ extern "C" {
 int ar_w4_matvec(const void *x, const void *q, const void *scales, int scales_type,
                  const void *zeros, int64_t m, int64_t N, int64_t K, int group, int act, void *out,
                  void *stream) {
-  return run_w4(x, 0, nullptr, m, 1, q, scales, scales_type, zeros, 1, N, K, group, act, out, false,
+  return run_w4(x, 0, nullptr, m, 1, q, scales, scales_type, zeros, 0, 1, N, K, group, act, out, false,
                 stream);
 }
 
 int ar_w4_matvec_experts(const void *x, int x_per_pair, const int32_t *ids, int64_t m, int k,
                          const void *q, const void *scales, int scales_type, const void *zeros,
-                         int E, int64_t N, int64_t K, int group, int act, void *out, void *stream) {
-  return run_w4(x, x_per_pair, ids, m, k, q, scales, scales_type, zeros, E, N, K, group, act, out,
-                true, stream);
+                         int first, int E, int64_t N, int64_t K, int group, int act, void *out,
+                         void *stream) {
+  return run_w4(x, x_per_pair, ids, m, k, q, scales, scales_type, zeros, first, E, N, K, group, act,
+                out, true, stream);
 }
 
 }  // extern "C"

@@ -75,6 +75,7 @@ struct W4Args {
   int64_t scale_count;  // scales, and zero points, of the whole array
   int pairs;        // rows of out
   int k;            // pair p takes row p / k of x
+  int first;        // number of q's first expert
   int E, N, K, ng;  // ng: groups of a row
   int width;        // columns of out: N, or N / 2 with the gated activation
   int act;
@@ -395,8 +396,9 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     for (int e = tid; e < 32 * each; e += threads) sets[e] = 0;
     __syncthreads();
     for (int p = tid; p < a.pairs; p += threads) {
-      const int e = __ldg(a.ids + p);
-      const bool ok = e >= 0 && e < a.E;
+      const int e = static_cast<int>(static_cast<uint32_t>(__ldg(a.ids + p)) -
+                                     static_cast<uint32_t>(a.first));
+      const bool ok = static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E);
       ids16[p] = static_cast<int16_t>(ok ? e : -1);
       if (ok) atomicAdd(&sets[e], 1);
     }
@@ -437,6 +439,17 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   }
   int item0, item1;
   w4_range(nsets * a.row_blocks, &item0, &item1);
+  // Checking build: the launch has the plan's warps and shared memory, whole
+  // teams, and room for a column set.
+  uint32_t dynamic_bytes;
+  asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dynamic_bytes));
+  if (!in_bounds(threads == static_cast<int>(blockDim.x) && warps <= kW4MaxWarps &&
+                     warps % a.team == 0 && a.cols <= 8 * NT && a.cols <= a.x_cols &&
+                     a.x_cols <= kW4MaxXCols &&
+                     static_cast<uint32_t>(a.smem_bytes) <= dynamic_bytes &&
+                     static_cast<int64_t>(nsets) * a.cols >= 0,
+                 a.status))
+    item1 = item0;
 
   // The expert of a column set.
   auto expert_of = [&](int set) -> int {

@@ -184,11 +184,13 @@ def ar_w4_matvec(x, q, scales, zeros=None, act="none", out=None, stream=None):
     return out
 
 
-def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", out=None, stream=None):
+def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", first=0, out=None,
+                         stream=None):
     """ar_w4_matvec with the weights of each token's experts: out [m, k, N]
     (or [m, k, N/2]) from x [m, K] (one row per token) or [m, k, K] (one per
-    choice), ids [m, k] int32 and q [E, N, K/2].  A row whose id lies outside
-    [0, E) is zero.  m * k <= 4096."""
+    choice), ids [m, k] int32 and q [E, N, K/2], experts first .. first + E -
+    1 of the layer.  A row whose id is none of these is zero.  m * k <=
+    4096."""
     dev = _device_of(x, "x")
     if not isinstance(ids, _TENSOR) or ids.dim() != 2:
         raise ValueError("ids must be a tensor [m, k]")
@@ -209,7 +211,7 @@ def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", out=None, st
     else:
         oa = _want(out, "out", _BF16, shape, dev)
     _call(_lib().ar_w4_matvec_experts, "ar_w4_matvec_experts", dev, stream, xa,
-          1 if per_pair else 0, ia, m, k, qa, sa, kind, za, q.shape[0], N, K, group, act, oa)
+          1 if per_pair else 0, ia, m, k, qa, sa, kind, za, first, q.shape[0], N, K, group, act, oa)
     return out
 
 

@@ -1108,6 +1108,38 @@ _ENV_MODES = {"0": "auto", "1": "one_stage", "2": "two_stage",
               "auto": "auto", "one_stage": "one_stage", "two_stage": "two_stage"}
 
 
+def run_experts(args):
+    """A decode step's expert layer (moe.ExpertLayer: 64 experts of 7168 x 2048
+    with 4-bit weights in groups of 128, 8 a token, one rank) from captured
+    graphs, one JSON line per batch size."""
+    import torch
+    from allreduce_sum_residual_gb300.moe import ExpertLayer
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    H, I, E, k = 7168, 2048, 64, 8
+    g = torch.Generator(device=dev)
+    g.manual_seed(0)
+
+    def w4(*lead, K):
+        q = torch.randint(0, 256, (*lead, K // 2), generator=g, device=dev, dtype=torch.uint8)
+        s = ((torch.rand((*lead, K // 128), generator=g, device=dev) + 0.5) / (4.6 * K ** 0.5)).bfloat16()
+        return q, s, None
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(shape, generator=g, device=dev) * std).bfloat16()
+
+    layer = ExpertLayer(normal(E, H, std=0.02), w4(E, 2 * I, K=H), w4(E, H, K=I), k)
+    weight = normal(H)
+    for m in (1, 2, 4, 8, 16, 32):
+        xs = [(normal(m, H), normal(m, H)) for _ in range(4)]
+        stream = torch.cuda.Stream()
+        us = 1e6 * graph_per_call(lambda c: layer(*xs[c % 4], weight, 1e-6), stream, 40, 10)
+        hit = len({e for x, _ in xs for e in layer.route(x)[1].flatten().tolist()})
+        print(json.dumps({"metric": "expert layer us/call", "value": us, "unit": "us", "rows": m,
+                          "experts": E, "experts_hit_by_4_batches": hit, "top_k": k, "hidden": H,
+                          "intermediate": I}), flush=True)
+
+
 def env_mode():
     v = os.environ.get("AR_MODE", "auto").strip().lower()
     if v not in _ENV_MODES:
@@ -1126,6 +1158,7 @@ def main(argv=None):
     ap.add_argument("--shapes", action="store_true", help="register-kernel launch-shape sweep")
     ap.add_argument("--kernels", action="store_true", help="register vs stream kernel sweep")
     ap.add_argument("--stream-shapes", action="store_true", help="stream-kernel shape sweep")
+    ap.add_argument("--experts", action="store_true", help="time a decode step's expert layer")
     ap.add_argument("--kernel-ns", default="1,2,3,4,8,16", help="--kernels: input counts")
     ap.add_argument("--kernel-hs", default="4096,7168", help="--kernels: hidden sizes")
     ap.add_argument("--kernel-ms", default="304,1024,4096,16384", help="--kernels: token counts")
@@ -1155,6 +1188,8 @@ def main(argv=None):
         return run_kernels(args)
     if args.stream_shapes:
         return run_stream_shapes(args)
+    if args.experts:
+        return run_experts(args)
     return run_ours(args)
 
 

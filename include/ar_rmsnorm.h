@@ -459,14 +459,16 @@ int ar_w4_matvec(const void *x, const void *q, const void *scales,
 
 /*
  * ar_w4_matvec with the weights of the routed experts:
- *   out[i, j, :] = x_ij * W[ids[i, j]]^T
+ *   out[i, j, :] = x_ij * W[ids[i, j] - first]^T
  * An expert's weights are read once for all its tokens (per 16 of them).
  * The pages have no counterpart of it.
  *   x            [m, K] bf16 with x_per_pair = 0 (every choice of a token
  *                takes the token's row), [m, k, K] with x_per_pair = 1.
- *   ids          [m, k] int32.  A value outside [0, E) is an expert that is
- *                not here (another rank's): its row of out is zero.  A token
- *                may name an expert twice.
+ *   ids          [m, k] int32, expert numbers of the whole layer.  One
+ *                outside [first, first + E) is an expert that is not here
+ *                (another rank's): its row of out is zero.  A token may name
+ *                an expert twice.
+ *   first        the number of the first expert that q holds, 0 or more.
  *   q, scales, zeros  as in ar_w4_matvec with a leading dimension E.
  *   m * k        at most AR_MATVEC_MAX_PAIRS; k <= AR_MAX_TOPK; E <=
  *                AR_MAX_EXPERTS.
@@ -475,8 +477,8 @@ int ar_w4_matvec(const void *x, const void *q, const void *scales,
  */
 int ar_w4_matvec_experts(const void *x, int x_per_pair, const int32_t *ids,
                          int64_t m, int k, const void *q, const void *scales,
-                         int scales_type, const void *zeros, int E, int64_t N,
-                         int64_t K, int group, int act, void *out,
+                         int scales_type, const void *zeros, int first, int E,
+                         int64_t N, int64_t K, int group, int act, void *out,
                          void *stream);
 
 /*

@@ -47,9 +47,10 @@ def w4(L, x=at(0), q=at(1), s=at(2), kind=1, z=at(3), m=4, N=64, K=256, group=64
     return L.ar_w4_matvec(x, q, s, kind, z, m, N, K, group, act, out, None)
 
 
-def w4e(L, x=at(0), per=0, ids=at(5), m=4, k=2, q=at(1), s=at(2), kind=1, z=at(3), E=8, N=64, K=256,
-        group=64, act=0, out=at(4)):
-    return L.ar_w4_matvec_experts(x, per, ids, m, k, q, s, kind, z, E, N, K, group, act, out, None)
+def w4e(L, x=at(0), per=0, ids=at(5), m=4, k=2, q=at(1), s=at(2), kind=1, z=at(3), first=0, E=8,
+        N=64, K=256, group=64, act=0, out=at(4)):
+    return L.ar_w4_matvec_experts(x, per, ids, m, k, q, s, kind, z, first, E, N, K, group, act, out,
+                                  None)
 
 
 W4_BOTH = [
@@ -70,7 +71,7 @@ def test_w4_matvec_refusals(arlib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", W4_BOTH + [
-    (dict(k=0), ARG), (dict(E=0), ARG), (dict(per=2), ARG), (dict(ids=0), ARG), (dict(k=17), UNSUPPORTED),
+    (dict(k=0), ARG), (dict(E=0), ARG), (dict(first=-1), ARG), (dict(per=2), ARG), (dict(ids=0), ARG), (dict(k=17), UNSUPPORTED),
     (dict(E=513), UNSUPPORTED), (dict(m=2049), UNSUPPORTED), (dict(ids=at(5) + 2), ALIGN),
     (dict(out=at(5)), ALIAS), (dict(per=1, out=at(0) + 4 * 256 * 2), ALIAS),
 ])

@@ -311,6 +311,21 @@ def test_w4_matvec_holds_over_the_range_of_x(level):
     ref.close(arn.ar_w4_matvec(x, q, s, zeros=z), *ref.product(x, q, s, z))
 
 
+def test_w4_matvec_experts_of_a_rank():
+    """`first`: the whole layer's numbers, of which this rank holds some."""
+    g = gen(15)
+    x = normal(g, 9, 256)
+    q, s, z = weights4(g, (12, 40), 256, 64, "bf16", True)
+    ids = torch.randint(-3, 15, (9, 4), generator=g, device=DEV, dtype=torch.int32)
+    ids[0, :2] = torch.tensor([-2 ** 31, 2 ** 31 - 1], dtype=torch.int32)
+    for first, count in ((0, 5), (5, 4), (9, 3)):
+        sl = slice(first, first + count)
+        got = arn.ar_w4_matvec_experts(x, ids, q[sl], s[sl], zeros=z[sl], first=first)
+        local = torch.where((ids >= first) & (ids < first + count), ids - first, -1).int()
+        ref.close(got, *expert_rows(x, local, q[sl], s[sl], z[sl], "none"))
+        assert not bool(got[local < 0].any())
+
+
 def test_w4_nan_and_infinite_rows_stay_their_own():
     """A NaN or an infinity in one row of x, or one scale, reaches no other
     row or output; the group behind a row's end takes no part."""
@@ -455,8 +470,8 @@ def test_ranks_partials_reach_the_epilogue():
         up = [None if t is None else t[sl] for t in inp["up"]]
         down = [None if t is None else t[sl] for t in inp["down"]]
         shared = inp["shared"] if rank == 0 else None
-        h = arn.ar_w4_matvec_experts(inp["x"], mine, *up, act="silu_mul")
-        y = arn.ar_w4_matvec_experts(h, mine, *down)
+        h = arn.ar_w4_matvec_experts(inp["x"], ids, *up, act="silu_mul", first=16 * rank)
+        y = arn.ar_w4_matvec_experts(h, ids, *down, first=16 * rank)
         ref.close(h, *expert_rows(inp["x"], mine, *up, "silu_mul"))
         ref.close(y, *expert_rows(h, mine, *down, "none"))
         assert not bool(y[mine < 0].any())
