@@ -566,36 +566,44 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       return xs + ((j >> 4) * a.x_cols + col) * 16 + (to ^ ((col & 1) << 2));
     };
     for (int col = warp / share; col < n; col += warps / share) {
-      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8);
-      int top = 0;
+      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + u0 * 16;
+      const int whole = min(pieces, a.K / 8 - u0 * 16);  // eights that the row has here
+      uint32_t tops = 0;  // the largest magnitudes of the even and of the odd elements
       for (int j = j0; j < pieces; j += 8 * step) {
         uint4 w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int at = j + i * step;
           w[i] = make_uint4(0, 0, 0, 0);
-          if (at < pieces && (u0 * 16 + at) * 8 < a.K) w[i] = __ldg(row + u0 * 16 + at);
+          if (at < whole) w[i] = __ldg(row + at);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int at = j + i * step;
           if (at >= pieces) break;
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {  // the upper 16 bits of an fp32 are a bf16
-            const int lo = v[e] << 16 & 0x7FFF0000, hi = v[e] & 0x7FFF0000;
-            top = max(top, lo < 0x7F800000 ? lo : 0);
-            top = max(top, hi < 0x7F800000 ? hi : 0);
-          }
-          *place(at, col) =
-              make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
-                         __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+          const uint4 v = w[i];
+          tops = __vmaxu2(tops, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          *place(at, col) = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
         }
       }
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      uint32_t top = max(tops & 0xFFFFu, tops >> 16);
+      if (top >= 0x7F80u) {  // an infinity or a NaN: the largest of the others
+        top = 0;
+        for (int j = j0; j < whole; j += step) {
+          const uint4 v = __ldg(row + j);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t h = e[i / 2] >> (i % 2 * 16) & 0x7FFFu;
+            if (h < 0x7F80u) top = max(top, h);
+          }
+        }
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top) << 16;  // a bf16 is the top half of an fp32
       if (lane == 0) {
-        if (share == 1) col_top[col] = top;
-        else atomicMax(&col_top[col], top);
+        if (share == 1) col_top[col] = static_cast<int>(top);
+        else atomicMax(&col_top[col], static_cast<int>(top));
       }
     }
     if (share > 1) __syncthreads();
