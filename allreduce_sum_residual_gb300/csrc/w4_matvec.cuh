@@ -388,13 +388,15 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   }
   if (tid < 20) nothing[tid] = make_uint4(0, 0, 0, 0);
   if (tid == 0) aborted = 0;
+  if constexpr (EXPERTS) {
+    for (int e = tid; e <= AR_MAX_EXPERTS; e += threads) sets[e] = 0;
+    __syncthreads();
+  }
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
   if constexpr (EXPERTS) {
     const int each = (a.E + 31) / 32;  // experts a lane counts up
-    for (int e = tid; e < 32 * each; e += threads) sets[e] = 0;
-    __syncthreads();
     for (int p = tid; p < a.pairs; p += threads) {
       const int e = static_cast<int>(static_cast<uint32_t>(__ldg(a.ids + p)) -
                                      static_cast<uint32_t>(a.first));
