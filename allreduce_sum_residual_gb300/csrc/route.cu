@@ -220,10 +220,22 @@ __device__ __noinline__ int order_row_exactly(const RouteArgs &a, const float (&
 
 // A score to a few 2^-24 of 1, in few instructions: ex2.approx is off by 2
 // ulp and its argument by half of one (of x - top or x, whose exponential or
-// derivative makes up for its size), rcp.approx by 1.
+// derivative makes up for its size), rcp.approx by 1; what they flush to zero
+// is below 2^-126.
+__device__ __forceinline__ float quick_exp2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float quick_inverse(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ float quick_score(const RouteArgs &a, float x, float top, float inv) {
-  if (a.softmax) return __expf(x - top) * inv;
-  return __fdividef(1.f, 1.f + __expf(-x));
+  constexpr float kLog2E = 1.44269504f;
+  if (a.softmax) return quick_exp2((x - top) * kLog2E) * inv;
+  return quick_inverse(1.f + quick_exp2(x * -kLog2E));
 }
 
 // A logit's order in the upper 23 bits, 2 or more; whole if it has 16.
@@ -275,15 +287,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
     if (b < INFINITY) reach = fmaxf(reach, b);  // an infinite choice is exact
   }
   if (a.bias != nullptr) reach = warp_max(reach);
-  // Keys in fixed point: `fine` steps in 1, from 3 (for -reach) on; a sum of
-  // two choices in half the steps.
-  const float fine = 8388590.f / (1.f + 2.f * reach), base = fmaf(reach, fine, 3.f);
+  // Keys in fixed point: `fine` steps in 1, from 3 (for -reach) on.  Adding
+  // 2^23 leaves the rounded steps in an fp32's lower 23 bits.
+  const float fine = 8388500.f / (1.f + 2.f * reach), base = fmaf(reach, fine, 3.f + 8388608.f);
   // How near two fp32 choices can be to come out in the wrong order.  In
   // 2^-24 of 1 + reach: a quick sigmoid is off by 6 at most, a softmax score
   // by 6 and its row's sum of up to 37 rounded adds, the sum with the bias by
   // 1, the key by 1.5 steps of 4: twice that is under 2^-19 and 2^-16.
   const float delta = (1.f + reach) * (a.softmax ? 0x1p-16f : 0x1p-19f);
   constexpr bool kExact = sizeof(T) == 2;  // keys that hold a logit whole
+  constexpr uint32_t kTop = 8388600u;
 
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); row < a.m;
        row += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
@@ -318,51 +331,41 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
       sc = scale_of<float, V>(x);
       inv = 1.f / sc.sum;
     }
-    // Choices (-inf: off) and keys.  0: no candidate; 1 in the upper bits:
-    // off; from 2 on the choices, as fixed point, or the logits' own order.
-    float c[V];
+    // Keys.  0: no candidate; 1 in the upper bits: off; from 2 on the
+    // choices, as fixed point (kTop: infinite), or the logits' own order.
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      uint32_t order;
+      uint32_t order;  // in the upper bits
+      bool on = x[i] > -INFINITY;
       if constexpr (LOGIT) {
-        c[i] = x[i];
         order = logit_order<kExact>(x[i]);
       } else {
-        c[i] = quick_score(a, x[i], sc.top, inv) + bias[i];
-        order = static_cast<uint32_t>(fminf(fmaf(c[i], fine, base), 8388600.f)) << 9;  // 2 or more
+        const float c = quick_score(a, x[i], sc.top, inv) + bias[i];
+        on = on && c > -INFINITY;
+        order = __float_as_uint(fminf(fmaf(c, fine, base), 8388608.f + kTop)) << 9;
       }
-      if (!(x[i] > -INFINITY) || !(c[i] > -INFINITY)) {
-        c[i] = -INFINITY;
-        order = 1u << 9;
-      }
-      key[i] = i < count ? order | static_cast<uint32_t>(511 - first - i) : 0u;
+      if (!on) order = 1u << 9;
+      key[i] = i < count ? order + static_cast<uint32_t>(511 - first - i) : 0u;
     }
     sort_keys<V>(key);
     bool close = false;
     bool kept = true;
     if (a.topk_groups < a.groups) {
-      float hi = -INFINITY, second = -INFINITY;  // the two largest choices
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float v = i < count ? c[i] : -INFINITY;
-        second = fmaxf(second, fminf(hi, v));
-        hi = fmaxf(hi, v);
-      }
+      uint32_t k1 = key[0], k2 = V > 1 ? key[1] : 0u;  // the group's two largest keys
       for (int o = 1; o < 1 << a.lanes_log2; o <<= 1) {
-        const float h = __shfl_xor_sync(0xFFFFFFFFu, hi, o);
-        const float s = __shfl_xor_sync(0xFFFFFFFFu, second, o);
-        second = fmaxf(fminf(hi, h), fmaxf(second, s));
-        hi = fmaxf(hi, h);
+        const uint32_t q1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o);
+        const uint32_t q2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
+        k2 = max(min(k1, q1), max(k2, q2));
+        k1 = max(k1, q1);
       }
-      // -inf with too few experts that are on
-      const float mine = !a.top2 ? hi : second > -INFINITY ? hi + second : -INFINITY;
+      // Twice the group's score in the keys' steps; 2 with too few experts
+      // that are on, 2 kTop with an infinite one.
+      const uint32_t o1 = k1 >> 9, o2 = a.top2 ? k2 >> 9 : o1;
+      uint32_t twice = o1 + (o1 == kTop ? o1 : o2);
+      if (min(o1, o2) <= 1u) twice = 2u;
       // The groups' keys, and as many rounds as groups are kept.
-      uint32_t order = 1u << 9;
-      if (mine > -INFINITY)
-        order = LOGIT ? logit_order<kExact>(mine)
-                      : static_cast<uint32_t>(fminf(fmaf(mine, 0.5f * fine, base), 8388600.f)) << 9;
-      uint32_t score = group < a.groups ? order | static_cast<uint32_t>(511 - group) : 0u;
+      uint32_t score = group < a.groups ? (twice >> 1) << 9 | static_cast<uint32_t>(511 - group) : 0u;
       kept = false;
       uint32_t best = 0u;
       for (int r = 0; r < a.topk_groups; ++r) {
@@ -382,9 +385,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
         } else {
           const int last_lane = (511 - static_cast<int>(best & 511u)) << a.lanes_log2;
           const int next_lane = (511 - static_cast<int>(next & 511u)) << a.lanes_log2;
-          const float above = __shfl_sync(0xFFFFFFFFu, mine, last_lane);
-          const float below = __shfl_sync(0xFFFFFFFFu, mine, next_lane);
-          close = !(above - below > delta + delta);
+          const uint32_t above = __shfl_sync(0xFFFFFFFFu, twice, last_lane);
+          const uint32_t below = __shfl_sync(0xFFFFFFFFu, twice, next_lane);
+          // 2 steps for the halves that the keys leave out, 2 to be over
+          // the line.
+          close = static_cast<float>(static_cast<int>(above - below)) <= 2.f * delta * fine + 4.f;
         }
       }
       if (!LOGIT && close && !a.softmax) {  // the same in every lane
@@ -468,10 +473,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
           const float bk = __shfl_sync(0xFFFFFFFFu, bs, a.k - 1);
           int rivals = 0;
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            rivals += kept && i < count && !(c[i] <= ck - delta) && c[i] > -INFINITY &&
+          for (int i = 0; i < V; ++i) {
+            const float c = x[i] > -INFINITY ? quick_score(a, x[i], sc.top, inv) + bias[i] : -INFINITY;
+            rivals += kept && i < count && !(c <= ck - delta) && c > -INFINITY &&
                               !(x[i] == xk && bias[i] == bk)
                           ? 1 : 0;
+          }
           const uint32_t found = __ballot_sync(
               0xFFFFFFFFu, lane <= a.k && order > 1u && !(cs <= ck - delta) && !(xs == xk && bs == bk));
           again |= a.softmax || static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rivals)) > __popc(found);
