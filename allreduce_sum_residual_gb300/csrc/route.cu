@@ -21,8 +21,8 @@
 // are.  Neighbours with the same logit and bias are exact ties, which need no
 // second look.
 //
-// Bound by instructions, some 450 a row of 256 experts: 16384 such rows with
-// groups and bias take 12 us (52 us with k passes over every lane's choices
+// Bound by instructions, some 770 a row of 256 experts: 16384 such rows with
+// groups and bias take 18.3 us (52 us with k passes over every lane's choices
 // in place of the keys), where their bytes would take 2.6 us.
 #include <cuda_fp16.h>
 
@@ -263,10 +263,15 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
           }
 }
 
-// LOGIT: a.by_logit.  Registers for eight CTAs an SM (four, two): the common
-// path fits, the second look spills.
+// CTAs an SM, by the registers: with six (80) the 16384 rows above take 18.3
+// us, with eight (64), where more than the second look spills, 19.8 us, with
+// five (96) 18.5 us.
+constexpr int route_ctas(int v) { return v <= 8 ? 6 : v == 16 ? 4 : 2; }
+
+// LOGIT: a.by_logit.
 template <typename T, int V, bool LOGIT>
-__global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2) k_route(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(V))
+    k_route(const __grid_constant__ RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int group = lane >> a.lanes_log2;
   const int in_group = (lane & ((1 << a.lanes_log2) - 1)) * V;
@@ -298,8 +303,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
   constexpr bool kExact = sizeof(T) == 2;  // keys that hold a logit whole
   constexpr uint32_t kTop = 8388600u;
 
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); row < a.m;
-       row += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
+       row += step) {
     const T *p = static_cast<const T *>(a.x) + row * a.stride;
     float x[V];
     if (a.vec) {
@@ -505,7 +511,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V == 16 ? 4 : 2
         }
       }
       if (again) {  // the same in every lane
-        id = order_row_exactly<V>(a, x, valid, first);
+        float copy[V];  // its address leaves this function: x stays in registers
+#pragma unroll
+        for (int i = 0; i < V; ++i) copy[i] = x[i];
+        id = order_row_exactly<V>(a, copy, valid, first);
         xs = id >= 0 ? to_float(p[id]) : -INFINITY;
       }
     }
@@ -617,7 +626,7 @@ extern "C" int ar_route_experts(const void *logits, int logits_type, int64_t row
                      : logits_type == AR_TYPE_BF16 ? route_kernel<__nv_bfloat16>(v, a.by_logit)
                                                    : route_kernel<__half>(v, a.by_logit);
   int64_t grid = (m + kRouteWarps - 1) / kRouteWarps;
-  const int64_t cap = static_cast<int64_t>(d->sms) * 8;  // the bias is read once a warp
+  const int64_t cap = static_cast<int64_t>(d->sms) * route_ctas(v);  // the bias is read once a warp
   if (grid > cap) grid = cap;
   return launch_pdl(kern, a, grid, kRouteWarps * 32, 0, 1, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
