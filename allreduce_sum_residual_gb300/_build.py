@@ -2,13 +2,17 @@
 
 Each .cu file compiles to an object in parallel; the objects link into
 ``allreduce_sum_residual_gb300/libarnorm.so``.  Only nvcc is needed (no
-cmake); the same command works on x86_64 and aarch64 hosts.
+cmake); the same command works on x86_64 and aarch64 hosts.  Beside it g++
+builds ``_binding.so``, the expert-layer calls on torch tensors, against the
+installed torch.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,8 @@ LIB = os.path.join(PKG, "libarnorm.so")
 # device status word and skips the access.  For tests, not for production.
 CHECK_OBJ_DIR = os.path.join(PKG, "_build_check")
 CHECK_LIB = os.path.join(PKG, "libarnorm_check.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -50,12 +56,38 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so unless it is newer than its sources and torch."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.join(torch, "version.py"),
+            os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), check: bool = False) -> str:
     """Compile and link libarnorm.so (with ``check``: libarnorm_check.so, the
-    checking build) unless it is newer than every source."""
+    checking build) unless it is newer than every source; without ``check``
+    _binding.so too."""
     lib_path, obj_dir = (CHECK_LIB, CHECK_OBJ_DIR) if check else (LIB, OBJ_DIR)
     extra_flags = tuple(extra_flags) + (("-DAR_CHECK=1",) if check else ())
     if not force and up_to_date(lib_path):
+        if not check:
+            build_binding()
         return lib_path
     os.makedirs(obj_dir, exist_ok=True)
     cc = nvcc()
@@ -71,13 +103,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), check: boo
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = None if check else ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, srcs))
     tmp = lib_path + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {os.path.basename(lib_path)} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if binding is not None:
+        binding.result()
     return lib_path
 
 

@@ -2,7 +2,13 @@
 with 4-bit weights, the weighted sum of the experts' outputs.
 
 Argument marshalling only, as in the package itself, which these functions
-are called through (``arn.ar_route_experts`` and so on)."""
+are called through (``arn.ar_route_experts`` and so on).  A call on the
+current stream goes through _binding.so, which checks, allocates and calls in
+one step; what that does not take (a given stream, another device than the
+current one, anything wrong) goes the long way here, which names what is
+wrong."""
+import ctypes
+
 import torch
 
 from . import (ACTS, AR_ACT_SILU_MUL, AR_TYPE_BF16, AR_TYPE_F16, AR_TYPE_F32, GROUP_SCORES,
@@ -14,9 +20,27 @@ _I32, _U8 = torch.int32, torch.uint8
 _empty = torch.empty
 _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-# What follows runs on every call of a decode step, where it costs more than
-# the kernels: one combined test per tensor, the reasons only when it fails,
-# devices by their number, and the stream's handle without its object.
+_native = None     # _binding.so
+_bound_to = None   # the library whose entry points it has
+
+
+def _fast():
+    """_binding.so, with the entry points of the loaded library."""
+    global _native, _bound_to
+    lib = _lib()
+    if lib is not _bound_to:
+        if _native is None:
+            try:
+                from . import _binding
+            except ImportError as e:
+                raise RuntimeError("_binding.so is not built: run `python -c \"import __graft_entry__ "
+                                   "as g; g.build()\"` (there is no fallback)") from e
+            _native = _binding
+        _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                       (lib.ar_route_experts, lib.ar_w4_matvec, lib.ar_w4_matvec_experts,
+                        lib.ar_combine, lib.ar_combine_rmsnorm)))
+        _bound_to = lib
+    return _native
 
 
 def _type_code(t, name):
@@ -103,6 +127,12 @@ def ar_route_experts(logits, k, bias=None, scoring="softmax", groups=1, topk_gro
     `groups` runs of experts are chosen.  renorm: divide the weights by
     their sum; scale: then multiply by this.
     Equal choices go to the lowest index, decided as in 64 bits."""
+    if stream is None:
+        r = _fast().route_experts(logits, k, bias, SCORES.get(scoring, scoring), groups, topk_groups,
+                                  GROUP_SCORES.get(group_score, group_score), renorm, scale,
+                                  weights, ids)
+        if r is not None:
+            return r
     dev = _device_of(logits, "logits")
     kind = _type_code(logits, "logits")
     if logits.dim() != 2:
@@ -165,6 +195,10 @@ def ar_w4_matvec(x, q, scales, zeros=None, act="none", out=None, stream=None):
     q: [N, K/2] uint8, the low four bits hold the even k.  scales: [N, K/G]
     float32, bfloat16 or float16 with groups of G = 32, 64 or 128.  zeros:
     [N, K/G] uint8, or None for a zero point of 8."""
+    if stream is None:
+        r = _fast().w4_matvec(x, q, scales, zeros, ACTS.get(act, act), out)
+        if r is not None:
+            return r
     dev = _device_of(x, "x")
     of_x = x.shape
     if len(of_x) != 2:
@@ -191,6 +225,10 @@ def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", first=0, out
     choice), ids [m, k] int32 and q [E, N, K/2], experts first .. first + E -
     1 of the layer.  A row whose id is none of these is zero.  m * k <=
     4096."""
+    if stream is None:
+        r = _fast().w4_matvec_experts(x, ids, q, scales, zeros, ACTS.get(act, act), first, out)
+        if r is not None:
+            return r
     dev = _device_of(x, "x")
     if not isinstance(ids, _TENSOR) or ids.dim() != 2:
         raise ValueError("ids must be a tensor [m, k]")
@@ -246,6 +284,10 @@ def ar_combine(y, weights, shared=None, slots=None, out=None, stream=None):
 
     y: [m, k, H], or [rows, H] with slots [m, k] int32 (a slot outside
     [0, rows) adds nothing).  weights: [m, k] float32.  shared: [m, H]."""
+    if stream is None:
+        r = _fast().combine(y, weights, shared, slots, out)
+        if r is not None:
+            return r
     dev, m, k, H, rows, ya, sa, wa, ha = _combine_operands(y, weights, shared, slots)
     shape = (m, H)
     if out is None:
@@ -262,6 +304,11 @@ def ar_combine_rmsnorm(y, weights, residual, weight, eps, shared=None, slots=Non
     """ar_combine's sum through the residual add and RMSNorm in one pass;
     residual, weight, eps and the outputs as in ar_rmsnorm.  Returns (out,
     residual_out)."""
+    if stream is None:
+        r = _fast().combine_rmsnorm(y, weights, residual, weight, eps, shared, slots, out,
+                                    residual_out)
+        if r is not None:
+            return r
     dev, m, k, H, rows, ya, sa, wa, ha = _combine_operands(y, weights, shared, slots)
     shape = (m, H)
     ra = _want(residual, "residual", _BF16, shape, dev)
