@@ -60,7 +60,7 @@ static int allow_shared_memory(int bytes) {
 }
 
 struct W4Plan {
-  int r, nt, warps, team, phase_units, cols, x_cols;
+  int r, nt, warps, team, units, phase_units, cols, x_cols;
   int64_t sets;    // most column sets
   int64_t rounds;  // items of a team, about
 };
@@ -69,10 +69,10 @@ struct W4Plan {
 // `most` (and no more than sets could fill); false if not even one set does.
 // `rounds`: items a team has to walk.
 static bool w4_layout(W4Plan *p, int group, int64_t rounds, int64_t most, bool experts, W4Args *a) {
-  const bool phased = p->phase_units < a->units;
-  const int64_t column = int64_t{p->phase_units} * 256;
+  const bool phased = p->phase_units < p->units;
+  const int64_t column = int64_t{p->phase_units} * w4_parts(p->r, p->nt, group) * 256;
   const int64_t tile = int64_t{p->cols} * 16 * p->r * 4;
-  const int64_t ring = int64_t{p->warps} * w4_depth(p->r) * w4_slot_bytes(p->r, group);
+  const int64_t ring = int64_t{p->warps} * w4_ring_bytes(p->r, p->nt, group);
   const int64_t red = p->team > 1 ? int64_t{2} * p->warps * tile : 0;
   const int teams = p->warps / p->team;
   // Sums between phases: as many items a team as 32 KB hold.
@@ -129,10 +129,12 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
     p.sets = experts ? a->E + a->pairs / p.cols : (a->pairs + p.cols - 1) / p.cols;
     if (p.sets > a->pairs) p.sets = a->pairs;
     const int64_t likely = experts && p.sets > a->E ? a->E : p.sets;
-    for (p.r = 1; p.r <= (group == 32 ? 1 : 2); ++p.r)
+    for (p.r = 1; p.r <= (group == 32 ? 1 : 2); ++p.r) {
+      const int parts = w4_parts(p.r, p.nt, group), unit_k = parts * kW4PartK;
+      p.units = (a->K + unit_k - 1) / unit_k;
       for (p.team = 1; p.team <= p.warps; p.team *= 2)
-        for (int phases = 1; phases <= a->units; ++phases) {
-          p.phase_units = (a->units + phases - 1) / phases;
+        for (int phases = 1; phases <= p.units; ++phases) {
+          p.phase_units = (p.units + phases - 1) / phases;
           const int64_t items = likely * ((a->width + per_row * p.r - 1) / (per_row * p.r));
           const int64_t each = (items + sms - 1) / sms;
           const int teams = p.warps / p.team;
@@ -143,7 +145,7 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
           double rate = p.r == 1 ? 27 : p.nt == 1 ? 34 : 30;
           if (busy < 12) rate *= busy < 8 ? busy / 12 : 0.67 + (busy - 8) / 12;
           const double chunks = phases == 1 ? 1 : (rounds + a->phase_rounds - 1) / a->phase_rounds;
-          const double time = n * p.r * a->units / rate +
+          const double time = n * p.r * p.units * parts / rate +
                               rounds * phases * (p.team == 1 ? 0.2 : 0.3 + 0.05 * p.team) +
                               chunks * (0.05 * p.cols * a->K / 512 + 1.5 * phases);
           if (!found || time < least) {
@@ -153,6 +155,7 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
           }
           break;
         }
+    }
   }
   if (found) w4_layout(best, group, best->rounds, most, experts, a);
   return found;
@@ -207,7 +210,6 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.scale_count = E * N * ng;
   a.width = static_cast<int>(width);
   a.act = act;
-  a.units = static_cast<int>((K + kW4UnitK - 1) / kW4UnitK);
   a.status = d->status;
 
   W4Plan p;
@@ -216,6 +218,7 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.x_cols = p.x_cols;
   a.warps = p.warps;
   a.team = p.team;
+  a.units = p.units;
   a.phase_units = p.phase_units;
   a.wait_limit_ns = kWaitLimitNs;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;

@@ -63,7 +63,13 @@
 namespace arn {
 
 constexpr int kW4MaxWarps = 16;  // four a scheduler, 128 registers a thread
-constexpr int kW4UnitK = 128;  // k of a unit
+constexpr int kW4PartK = 128;  // k of a unit's part
+// Parts of a unit.  Two where one row tile and one column tile leave little
+// to do for a unit's fixed work (one row, 7168 x 7168: 10.7 us instead of 11.4);
+// not with two column tiles or groups of 32, whose x or scales need the room.
+__host__ __device__ constexpr int w4_parts(int r, int nt, int group) {
+  return r == 1 && nt == 1 && group != 32 ? 2 : 1;
+}
 
 struct W4Args {
   const uint4 *x;      // rows of K bf16
@@ -79,7 +85,7 @@ struct W4Args {
   int E, N, K, ng;  // ng: groups of a row
   int width;        // columns of out: N, or N / 2 with the gated activation
   int act;
-  int units;        // units of a row: ceil(K / 128)
+  int units;        // units of a row: ceil(K / (128 parts))
   int row_blocks;   // items of a column set
   int cols;         // most columns of a set
   int x_cols;       // columns of x that shared memory holds (at least cols)
@@ -96,14 +102,19 @@ constexpr int kW4MaxSets = 32;   // column sets staged at a time
 constexpr int kW4MaxXCols = 64;  // columns staged at a time
 
 // Units of a warp's ring: 64 KB in flight an SM behind those in use.
-__host__ __device__ constexpr int w4_depth(int r) { return r == 1 ? 5 : 3; }
+__host__ __device__ constexpr int w4_depth(int r, int nt, int group) {
+  return r * w4_parts(r, nt, group) == 1 ? 5 : 3;
+}
 __host__ __device__ constexpr int w4_row_bytes(int group) {
   return group == 32 ? 112 : group == 64 ? 96 : 64;
 }
 // Scales and zero points of a row: behind its weights, or with groups of 128
-// behind the unit's.
-__host__ __device__ constexpr int w4_slot_bytes(int r, int group) {
+// behind the part's.
+__host__ __device__ constexpr int w4_part_bytes(int r, int group) {
   return 16 * r * (w4_row_bytes(group) + (group == 128 ? 8 : 0));
+}
+__host__ __device__ constexpr int w4_ring_bytes(int r, int nt, int group) {
+  return w4_depth(r, nt, group) * w4_parts(r, nt, group) * w4_part_bytes(r, group);
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
@@ -322,9 +333,11 @@ struct W4Walk {
 template <int R, int NT, int G, int ST, bool ZEROS, bool EXPERTS>
 __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(16) unsigned char w4_smem[];
-  constexpr int kDepth = w4_depth(R), kSlot = w4_slot_bytes(R, G);
+  constexpr int kDepth = w4_depth(R, NT, G), kParts = w4_parts(R, NT, G);
+  constexpr int kPart = w4_part_bytes(R, G), kSlot = kParts * kPart;
+  static_assert(kDepth * kSlot == w4_ring_bytes(R, NT, G), "the ring that the plan laid out");
   constexpr int kRowBytes = w4_row_bytes(G);
-  constexpr int kGroups = kW4UnitK / G;  // groups of a unit
+  constexpr int kGroups = kW4PartK / G;  // groups of a part
   constexpr int kRows = 16 * R;
   // Of local row lr: its scale words at lr * kScaleStride + kScaleAt, its
   // zero points kZeroAt behind them.
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   constexpr int kScaleStride = G == 128 ? 8 : kRowBytes;
   constexpr int kZeroAt = G == 128 ? 4 : G == 64 ? 8 : 32;
   constexpr int kScaleBytes = ST == AR_TYPE_F32 ? 4 : 2;
-  // Aligned words that hold a unit's scales, or zero points, of one row.
+  // Aligned words that hold a part's scales, or zero points, of one row.
   constexpr int kScaleWords = ST == AR_TYPE_F32 ? kGroups : kGroups == 1 ? 1 : kGroups / 2 + 1;
   constexpr int kZeroWords = kGroups == 1 ? 1 : 2;
 
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       const int block = item % a.row_blocks;
       const int64_t row_bytes = a.K / 2;
       for (int d = 0, u = member; d < kDepth - 1 && u < a.phase_units; ++d, u += a.team) {
-        const int64_t piece = static_cast<int64_t>(u) * 64 + t * 16;
+        const int64_t piece = static_cast<int64_t>(u) * (64 * kParts) + t * (16 * kParts);
 #pragma unroll
         for (int i = 0; i < 2 * R; ++i)
           if (piece < row_bytes)
@@ -477,7 +490,10 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   int64_t f_first = 0;           // first row of W of the set's expert
   const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the unit in the expert's first row
   uint32_t f_off[2 * R];         // the rows' distances, in 16 bytes
-  const uint8_t *f_s = nullptr, *f_z = nullptr;  // the unit's scales and zero points of row `lane`
+  // The unit's scales and zero points of one row of a part: part lane / 16
+  // (one row tile) or row `lane`.
+  const int s_part = kParts > 1 ? lane / kRows : 0;
+  const uint8_t *f_s = nullptr, *f_z = nullptr;
   bool f_plain = false;          // neither ends inside a unit nor near the end of its arrays
   uint32_t f_slot = ring;
   // Points at the rows of the walk's item and takes its units.
@@ -489,15 +505,16 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     }
     f_unit = walk.unit;
     to_come = (walk.u1 - walk.unit + a.team - 1) / a.team;
-    f_q = a.q + f_first * row_bytes + t * 16 + f_unit * 64;
+    f_q = a.q + f_first * row_bytes + t * 16 + f_unit * (64 * kParts);
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i)
       f_off[i] = static_cast<uint32_t>(w4_row<R>(a, block, g + 8 * i)) *
                  static_cast<uint32_t>(row_bytes >> 4);
-    const int64_t el = (f_first + w4_row<R>(a, block, lane & (kRows - 1))) * a.ng + f_unit * kGroups;
+    const int64_t el = (f_first + w4_row<R>(a, block, lane & (kRows - 1))) * a.ng +
+                       (f_unit * kParts + s_part) * kGroups;
     f_s = a.scales + el * kScaleBytes;
     if constexpr (ZEROS) f_z = a.zeros + el;
-    f_plain = __all_sync(0xFFFFFFFFu, el + a.ng + 16 <= a.scale_count) && a.K % kW4UnitK == 0;
+    f_plain = __all_sync(0xFFFFFFFFu, el + a.ng + 16 <= a.scale_count) && a.K % (kParts * kW4PartK) == 0;
     walk.unit += to_come * a.team;
     walk.settle(a);
   };
@@ -509,13 +526,16 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     if (to_come > 0) {
       --to_come;
       const uint32_t to = f_slot + g * kRowBytes + t * 16;
-      const uint32_t to_s = f_slot + kScaleAt + lane * kScaleStride;
+      const uint32_t to_s = f_slot + s_part * kPart + kScaleAt + (lane & (kRows - 1)) * kScaleStride;
       const uint8_t *ws = word_of(f_s), *wz = word_of(f_z);
       if (f_plain) {
 #pragma unroll
         for (int i = 0; i < 2 * R; ++i)
-          cp_async_16(to + 8 * i * kRowBytes, f_q + static_cast<uint64_t>(f_off[i]) * 16);
-        if (kRows == 32 || lane < kRows) {
+#pragma unroll
+          for (int j = 0; j < kParts; ++j)
+            cp_async_16(to + j * kPart + 8 * i * kRowBytes,
+                        f_q + static_cast<uint64_t>(f_off[i]) * 16 + j * 64);
+        if (kParts * kRows == 32 || lane < kRows) {
 #pragma unroll
           for (int i = 0; i < kScaleWords; ++i) cp_async_4(to_s + 4 * i, ws + 4 * i);
           if constexpr (ZEROS) {
@@ -525,27 +545,31 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
         }
       } else {
         // Zeros behind the row's end; words cut off at the end of the arrays.
-        const bool here = f_unit * 64 + t * 16 < static_cast<int>(row_bytes);
 #pragma unroll
-        for (int i = 0; i < 2 * R; ++i)
-          cp_async_16_of(to + 8 * i * kRowBytes,
-                         here ? f_q + static_cast<uint64_t>(f_off[i]) * 16 : a.q, here ? 16u : 0u);
-        if (lane < kRows) {
-          auto words = [&](uint32_t dst, const uint8_t *w, const uint8_t *end, int n) {
-            for (int i = 0; i < n; ++i) {
-              const int64_t left = end - (w + 4 * i);
-              if (left > 0)
-                cp_async_4_of(dst + 4 * i, w + 4 * i, left < 4 ? static_cast<uint32_t>(left) : 4u);
-            }
-          };
+        for (int j = 0; j < kParts; ++j) {
+          const bool here = (f_unit * kParts + j) * 64 + t * 16 < static_cast<int>(row_bytes);
+#pragma unroll
+          for (int i = 0; i < 2 * R; ++i)
+            cp_async_16_of(to + j * kPart + 8 * i * kRowBytes,
+                           here ? f_q + static_cast<uint64_t>(f_off[i]) * 16 + j * 64 : a.q,
+                           here ? 16u : 0u);
+        }
+        auto words = [&](uint32_t dst, const uint8_t *w, const uint8_t *end, int n) {
+          for (int i = 0; i < n; ++i) {
+            const int64_t left = end - (w + 4 * i);
+            if (left > 0)
+              cp_async_4_of(dst + 4 * i, w + 4 * i, left < 4 ? static_cast<uint32_t>(left) : 4u);
+          }
+        };
+        if (kParts * kRows == 32 || lane < kRows) {
           words(to_s, ws, a.scales + a.scale_count * kScaleBytes, kScaleWords);
           if constexpr (ZEROS) words(to_s + kZeroAt, wz, a.zeros + a.scale_count, kZeroWords);
         }
       }
       f_unit += a.team;
-      f_q += a.team * 64;
-      f_s += a.team * (kGroups * kScaleBytes);
-      if constexpr (ZEROS) f_z += a.team * kGroups;
+      f_q += a.team * (64 * kParts);
+      f_s += a.team * (kParts * kGroups * kScaleBytes);
+      if constexpr (ZEROS) f_z += a.team * (kParts * kGroups);
       f_slot += kSlot;
       if (f_slot == ring + kDepth * kSlot) f_slot = ring;
     }
@@ -555,12 +579,13 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   for (int i = 0; i < kDepth - 1; ++i) fetch();
 
   // Units [u0, u1) of the first n columns into shared memory, as fp16 times
-  // their powers of two: [unit][column][step][lane], odd columns with the
+  // their powers of two: [part][column][step][lane], odd columns with the
   // steps of a pair exchanged (no bank conflicts between two columns).  A
   // column's eights go to one warp, or to as many as there are for it; eight
   // loads of a lane are under way at a time.
   auto stage = [&](int u0, int u1, int n) {
-    const int pieces = (u1 - u0) * 16;  // eights of a column
+    const int pieces = (u1 - u0) * (16 * kParts);  // eights of a column
+    const int before = u0 * (16 * kParts);
     const int share = n < warps ? warps / n : 1;  // warps of a column
     const int step = share * 32, j0 = warp % share * 32 + lane;
     auto place = [&](int j, int col) -> uint4 * {
@@ -568,8 +593,8 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       return xs + ((j >> 4) * a.x_cols + col) * 16 + (to ^ ((col & 1) << 2));
     };
     for (int col = warp / share; col < n; col += warps / share) {
-      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + u0 * 16;
-      const int whole = min(pieces, a.K / 8 - u0 * 16);  // eights that the row has here
+      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + before;
+      const int whole = min(pieces, a.K / 8 - before);  // eights that the row has here
       uint32_t tops = 0;  // the largest magnitudes of the even and of the odd elements
       for (int j = j0; j < pieces; j += 8 * step) {
         uint4 w[8];
@@ -759,69 +784,73 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
             cp_async_wait<kDepth - 2>();
             __syncwarp();  // every lane's copies are here, and the slot before is free
             fetch();
-            uint4 b[4][NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t off = c_unit * xstep[n];
-              b[0][n] = lds_128(xe[n] + off);
-              b[1][n] = lds_128(xo[n] + off + 64);
-              b[2][n] = lds_128(xe[n] + off + 128);
-              b[3][n] = lds_128(xo[n] + off + 192);
-            }
-            const int group0 = (u0 + c_unit) * kGroups;
+            for (int j = 0; j < kParts; ++j) {
+              const uint32_t part = slot + j * kPart;
+              uint4 b[4][NT];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              uint32_t w0[4], w1[4];
-              load_words<G>(w0, slot + (r * 16 + g) * kRowBytes, t);
-              load_words<G>(w1, slot + (r * 16 + 8 + g) * kRowBytes, t);
-              const uint32_t sc = slot + kScaleAt + (r * 16 + g) * kScaleStride;
+              for (int n = 0; n < NT; ++n) {
+                const uint32_t off = (c_unit * kParts + j) * xstep[n];
+                b[0][n] = lds_128(xe[n] + off);
+                b[1][n] = lds_128(xo[n] + off + 64);
+                b[2][n] = lds_128(xe[n] + off + 128);
+                b[3][n] = lds_128(xo[n] + off + 192);
+              }
+              const int group0 = ((u0 + c_unit) * kParts + j) * kGroups;
 #pragma unroll
-              for (int gi = 0; gi < kGroups; ++gi) {
-                // Scale and zero point of the two rows' group.
-                float s[2];
-                Offsets o[2];
+              for (int r = 0; r < R; ++r) {
+                uint32_t w0[4], w1[4];
+                load_words<G>(w0, part + (r * 16 + g) * kRowBytes, t);
+                load_words<G>(w1, part + (r * 16 + 8 + g) * kRowBytes, t);
+                const uint32_t sc = part + kScaleAt + (r * 16 + g) * kScaleStride;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t p = sc + h * 8 * kScaleStride;
-                  const int low = el_low[r][h] + group0;
-                  if constexpr (ST == AR_TYPE_F32) {
-                    s[h] = __uint_as_float(lds_32(p + gi * 4));
-                  } else if constexpr (G == 128) {
-                    // The upper or the lower half of the word, as the upper one.
-                    const uint32_t v = __byte_perm(lds_32(p), 0, (low & 1) * 0x2200 + 0x1044);
-                    s[h] = ST == AR_TYPE_BF16
-                               ? __uint_as_float(v)
-                               : __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
-                  } else {
-                    const uint32_t v = lds_16(p + (el_low[r][h] & 1) * 2 + gi * 2);
-                    s[h] = ST == AR_TYPE_BF16
-                               ? __uint_as_float(v << 16)
-                               : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+                for (int gi = 0; gi < kGroups; ++gi) {
+                  // Scale and zero point of the two rows' group.
+                  float s[2];
+                  Offsets o[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t p = sc + h * 8 * kScaleStride;
+                    const int low = el_low[r][h] + group0;
+                    if constexpr (ST == AR_TYPE_F32) {
+                      s[h] = __uint_as_float(lds_32(p + gi * 4));
+                    } else if constexpr (G == 128) {
+                      // The upper or the lower half of the word, as the upper one.
+                      const uint32_t v = __byte_perm(lds_32(p), 0, (low & 1) * 0x2200 + 0x1044);
+                      s[h] = ST == AR_TYPE_BF16
+                                 ? __uint_as_float(v)
+                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
+                    } else {
+                      const uint32_t v = lds_16(p + (el_low[r][h] & 1) * 2 + gi * 2);
+                      s[h] = ST == AR_TYPE_BF16
+                                 ? __uint_as_float(v << 16)
+                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+                    }
+                    // Behind the row's end stands another row's scale.
+                    if (kParts * kGroups > 1 && group0 + gi >= a.ng) s[h] = 0.f;
+                    o[h] = offsets_of(ZEROS ? lds_8(p + kZeroAt + (low & 3) + gi) & 15u : 8u);
                   }
-                  // Behind the row's end stands another row's scale.
-                  if (kGroups > 1 && group0 + gi >= a.ng) s[h] = 0.f;
-                  o[h] = offsets_of(ZEROS ? lds_8(p + kZeroAt + (low & 3) + gi) & 15u : 8u);
-                }
-                float d[NT][4];
-                constexpr int kSteps = 4 / kGroups;
+                  float d[NT][4];
+                  constexpr int kSteps = 4 / kGroups;
 #pragma unroll
-                for (int i = gi * kSteps; i < (gi + 1) * kSteps; ++i) {
-                  uint32_t p[4], q[4];
-                  unpack_word(p, w0[i], o[0]);
-                  unpack_word(q, w1[i], o[1]);
+                  for (int i = gi * kSteps; i < (gi + 1) * kSteps; ++i) {
+                    uint32_t p[4], q[4];
+                    unpack_word(p, w0[i], o[0]);
+                    unpack_word(q, w1[i], o[1]);
 #pragma unroll
-                  for (int n = 0; n < NT; ++n) {
-                    if (i == gi * kSteps)
-                      mma_first(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
-                    else
-                      mma_next(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
-                    mma_next(d[n], p[2], q[2], p[3], q[3], b[i][n].z, b[i][n].w);
+                    for (int n = 0; n < NT; ++n) {
+                      if (i == gi * kSteps)
+                        mma_first(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
+                      else
+                        mma_next(d[n], p[0], q[0], p[1], q[1], b[i][n].x, b[i][n].y);
+                      mma_next(d[n], p[2], q[2], p[3], q[3], b[i][n].z, b[i][n].w);
+                    }
                   }
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[r][n][c] = fmaf(s[c >> 1], d[n][c], acc[r][n][c]);
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) acc[r][n][c] = fmaf(s[c >> 1], d[n][c], acc[r][n][c]);
               }
             }
             slot += kSlot;
