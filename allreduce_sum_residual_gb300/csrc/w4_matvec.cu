@@ -102,15 +102,16 @@ static bool w4_layout(W4Plan *p, int group, int64_t rounds, int64_t most, bool e
 
 // The launch shape: row tiles and team that minimise an estimate of a CTA's
 // time, with the fewest phases whose x fits.
-//   - The CTA with most items goes through them at 27 KB/us with one row tile
-//     (16 x 6144 x 32768 with the activation: 48 us against 50 us with two),
+//   - The CTA with most items goes through them at 27 KB/us with one row tile,
 //     34 KB/us with two and one column tile (32 tokens, 112 experts of 1024 x
-//     6144: 77 us against 97 us): two read x half as often, but leave more to
-//     the last wave (one row, 7168 x 7168: 12.7 us against 11.9 us).
+//     6144: 76 us against 86 us): two read x half as often, but leave more to
+//     the last wave (one row, 7168 x 7168: 12.2 us against 10.7 us), and take
+//     room that x needs (16 x 6144 x 32768 with the activation: three phases
+//     in place of two).
 //   - Warps that find no item idle; twelve busy ones of sixteen reach most of
 //     that rate, eight two thirds of it.
 //   - An item's end costs a team of one 0.2 us, larger teams 0.4 to 1.1 us
-//     (the same 7168 x 7168: 11.9, 13.6 and 14.7 us with teams of 4, 8, 16).
+//     (the same 7168 x 7168: 10.7 and 11.8 us with teams of 4 and 8).
 //   - x takes 0.05 us a KB to unpack and 1.5 us a phase, for every chunk.
 static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
                     W4Plan *best) {

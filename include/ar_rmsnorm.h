@@ -436,10 +436,14 @@ int ar_route_experts(const void *logits, int logits_type, int64_t row_stride,
 /*
  * out[i, n] = bf16( sum_k x[i, k] W[n, k] ),  or its gated half (act), with
  *   W[n, k] = (q[n, k] - z[n, k / group]) * s[n, k / group]
- * for a decode batch of m rows: the weights are read once per 16 rows, at
- * the speed of memory.  Products are summed in fp32; s multiplies the fp32
- * sum of its group; one rounding, at the end.  The pages have no counterpart
- * of it.
+ * for a decode batch of m rows: the weights are read once per 8 or 16 rows.
+ * Products are summed in fp32; s multiplies the fp32 sum of its group; one
+ * rounding, at the end.  x enters the products as fp16 times a power of two
+ * of its row: exact down to 2^-30 of the row's largest finite magnitude,
+ * smaller ones to within 2^-38 of it.  The order of the fp32 sums depends on
+ * the shape and the device, not on the data, so equal calls give equal bits,
+ * and a row of another batch the same up to fp32 rounding.  The pages have no
+ * counterpart of it.
  *   x        [m, K] bf16.  m <= AR_MATVEC_MAX_ROWS.
  *   q        [N, K/2] bytes, two weights each: the low four bits hold the
  *            even k.
@@ -460,8 +464,10 @@ int ar_w4_matvec(const void *x, const void *q, const void *scales,
 /*
  * ar_w4_matvec with the weights of the routed experts:
  *   out[i, j, :] = x_ij * W[ids[i, j] - first]^T
- * An expert's weights are read once for all its tokens (per 16 of them).
- * The pages have no counterpart of it.
+ * An expert's weights are read once for all its tokens (per 8 of them, or 16
+ * where more than six an expert are the rule).  The order of the fp32 sums of
+ * a row depends on the ids of the batch; equal calls give equal bits.  The
+ * pages have no counterpart of it.
  *   x            [m, K] bf16 with x_per_pair = 0 (every choice of a token
  *                takes the token's row), [m, k, K] with x_per_pair = 1.
  *   ids          [m, k] int32, expert numbers of the whole layer.  One
