@@ -56,9 +56,13 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile _binding.so unless it is newer than its sources and torch."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def build_binding(force: bool = False):
+    """Compile _binding.so unless it is newer than its sources and torch (not
+    without torch: the C library needs none)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.join(torch, "version.py"),
             os.path.abspath(__file__)]
     if not force and os.path.exists(BINDING) and \
