@@ -1,6 +1,7 @@
 // ar_w4_matvec and ar_w4_matvec_experts: checks and the launch shape.  The
 // kernels (w4_matvec.cuh) are compiled in w4_<scale type>_<zero points: z or
 // n><experts: e or d>.cu.
+#include <cmath>
 #include <mutex>
 
 #include "w4_matvec.cuh"
@@ -60,30 +61,36 @@ static int allow_shared_memory(int bytes) {
 }
 
 struct W4Plan {
-  int r, nt, warps, team, units, phase_units, cols, x_cols;
-  int64_t sets;    // most column sets
+  int r, nt, warps, team, units, phases, phase_units, cols, x_cols;
   int64_t rounds;  // items of a team, about
 };
 
-// Lays out shared memory for a plan, with as many columns of x as fit into
-// `most` (and no more than sets could fill); false if not even one set does.
-// `rounds`: items a team has to walk.
-static bool w4_layout(W4Plan *p, int group, int64_t rounds, int64_t most, bool experts, W4Args *a) {
-  const bool phased = p->phase_units < p->units;
-  const int64_t column = int64_t{p->phase_units} * w4_parts(p->r, p->nt, group) * 256;
+// Lays out shared memory for a plan: the fewest phases (of p->units) with
+// which x of a set fits into `most`, and as many columns of x as do (no more
+// than the sets could fill); false if not even a unit's fits.
+static bool w4_layout(W4Plan *p, int group, int64_t most, bool experts, W4Args *a) {
+  const int64_t unit = int64_t{w4_parts(p->r, p->nt, group)} * 256;  // x of a unit's column
   const int64_t tile = int64_t{p->cols} * 16 * p->r * 4;
   const int64_t ring = int64_t{p->warps} * w4_ring_bytes(p->r, p->nt, group);
   const int64_t red = p->team > 1 ? int64_t{2} * p->warps * tile : 0;
+  const int64_t ids = experts ? (int64_t{2} * a->pairs + 15) / 16 * 16 : 0;
   const int teams = p->warps / p->team;
   // Sums between phases: as many items a team as 32 KB hold.
   a->phase_rounds = static_cast<int>(32768 / (teams * tile));
-  if (a->phase_rounds > rounds) a->phase_rounds = static_cast<int>(rounds);
+  if (a->phase_rounds > p->rounds) a->phase_rounds = static_cast<int>(p->rounds);
   if (a->phase_rounds < 1) a->phase_rounds = 1;
-  const int64_t acc = phased ? a->phase_rounds * teams * tile : 0;
-  const int64_t ids = experts ? (int64_t{2} * a->pairs + 15) / 16 * 16 : 0;
-  int64_t x_cols = (most - ring - red - acc - ids) / column;
-  if (x_cols < p->cols) return false;
-  if (phased) x_cols = p->cols;  // a phase holds one set
+  int64_t room = most - ring - red - ids, acc = 0;  // for x
+  p->phases = 1;
+  if (p->cols * p->units * unit > room) {
+    acc = a->phase_rounds * teams * tile;
+    room -= acc;
+    const int64_t fit = room < 0 ? 0 : room / (p->cols * unit);
+    if (fit < 1) return false;
+    p->phases = static_cast<int>((p->units + fit - 1) / fit);
+  }
+  p->phase_units = (p->units + p->phases - 1) / p->phases;
+  const int64_t column = p->phase_units * unit;
+  int64_t x_cols = p->phases > 1 ? p->cols : room / column;  // a phase holds one set
   if (x_cols > kW4MaxXCols) x_cols = kW4MaxXCols;
   if (x_cols > a->pairs) x_cols = a->pairs;
   p->x_cols = static_cast<int>(x_cols);
@@ -100,19 +107,45 @@ static bool w4_layout(W4Plan *p, int group, int64_t rounds, int64_t most, bool e
   return true;
 }
 
-// The launch shape: row tiles and team that minimise an estimate of a CTA's
-// time, with the fewest phases whose x fits.
-//   - The CTA with most items goes through them at 27 KB/us with one row tile,
-//     34 KB/us with two and one column tile (32 tokens, 112 experts of 1024 x
-//     6144: 76 us against 86 us): two read x half as often, but leave more to
-//     the last wave (one row, 7168 x 7168: 12.2 us against 10.7 us), and take
-//     room that x needs (16 x 6144 x 32768 with the activation: three phases
-//     in place of two).
-//   - Warps that find no item idle; twelve busy ones of sixteen reach most of
-//     that rate, eight two thirds of it.
-//   - An item's end costs a team of one 0.2 us, larger teams 0.4 to 1.1 us
-//     (the same 7168 x 7168: 10.7 and 11.8 us with teams of 4 and 8).
-//   - x takes 0.05 us a KB to unpack and 1.5 us a phase, for every chunk.
+// How many of E experts with `pairs` choices have more than n tokens, n < 64,
+// if their numbers are Poisson (0 from `end` on: too few to count).
+struct Crowds {
+  double above[64];
+  int end;
+  Crowds(int E, double mean) {
+    double p = exp(-mean), rest = 1 - p;
+    for (end = 0; end < 64 && rest > 1e-3;) {
+      above[end] = E * rest;
+      p *= mean / ++end;
+      rest -= p;
+    }
+  }
+  // Column sets of all experts: one for more than 0, cols, 2 cols, ... tokens.
+  double sets(int cols) const {
+    double s = 0;
+    for (int n = 0; n < end; n += cols) s += above[n];
+    return s;
+  }
+};
+
+// The launch shape: row and column tiles, team, columns of a set and phases
+// that minimise an estimate of a CTA's time.
+//   - Teams go through their items in rounds.  A round with all warps at work
+//     takes in 41 KB/us with one row tile and one column tile; somewhat more
+//     with two row tiles where rows are short (32 tokens, 112 experts of 1024
+//     x 6144: 76 us against 86 us) and less where they are long (4 tokens, 25
+//     of 64 experts of 7168 x 4096, gated: 109 us against 90 us); 27 KB/us
+//     with two column tiles (16 x 2048 x 32768: 17.4 us, where one reads the
+//     weights twice in 19.9 us).  A last round of few warps is not much
+//     faster than their share.
+//   - The end of a round costs 2 us, with the joined sums of larger teams 2.8
+//     us (1 x 7168 x 7168: 14.4, 11.8, 10.7 and 11.8 us with teams of 1, 2, 4
+//     and 8).
+//   - x takes 0.021 us a KB to unpack, and 2.2 us each time.  Experts, which
+//     seldom have all the columns that a set could, take a few less where
+//     that spares the phases (16 tokens of 7168, 8 of 64 experts: 7 columns
+//     in 176 us, 8 in 199 us).
+// Over 45 shapes the choice is within 2 % of the best shape on average.
 static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W4Args *a,
                     W4Plan *best) {
   double least = 0;
@@ -120,45 +153,54 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
   W4Plan p = {};
   p.warps = kW4MaxWarps;
   const int per_row = a->act == AR_ACT_SILU_MUL ? 8 : 16;  // outputs of a row tile
-  // Two column tiles where sets of more than eight are the rule.
-  for (p.nt = experts ? (a->pairs > 6 * a->E ? 2 : 1) : (m > 8 ? 2 : 1); p.nt >= 1 && !found;
-       --p.nt) {
-    // A set's columns: at most the batch, whose tokens seldom name an expert
-    // twice (that one then gets two sets).
-    p.cols = static_cast<int>(m < 8 * p.nt ? m : 8 * p.nt);
-    // Each set has an expert of its own or is full.
-    p.sets = experts ? a->E + a->pairs / p.cols : (a->pairs + p.cols - 1) / p.cols;
-    if (p.sets > a->pairs) p.sets = a->pairs;
-    const int64_t likely = experts && p.sets > a->E ? a->E : p.sets;
-    for (p.r = 1; p.r <= (group == 32 ? 1 : 2); ++p.r) {
-      const int parts = w4_parts(p.r, p.nt, group), unit_k = parts * kW4PartK;
-      p.units = (a->K + unit_k - 1) / unit_k;
-      for (p.team = 1; p.team <= p.warps; p.team *= 2)
-        for (int phases = 1; phases <= p.units; ++phases) {
-          p.phase_units = (p.units + phases - 1) / phases;
-          const int64_t items = likely * ((a->width + per_row * p.r - 1) / (per_row * p.r));
-          const int64_t each = (items + sms - 1) / sms;
+  const double mean = static_cast<double>(a->pairs) / a->E;
+  const Crowds crowds(a->E, experts && mean <= 16 ? mean : 0);
+  // Two column tiles for experts only where they fill them (64 tokens, 16 an
+  // expert, of 4096 x 4096, gated: 54 us against 44 us).
+  const int most_nt = m > 8 && (!experts || mean > 16) ? 2 : 1;
+  for (p.nt = 1; p.nt <= most_nt; ++p.nt) {
+    const int widest = static_cast<int>(m < 8 * p.nt ? m : 8 * p.nt);
+    bool whole = false;  // a plan of one phase
+    for (p.cols = widest; p.cols > (experts ? widest / 2 : widest - 1) && !whole; --p.cols) {
+      const double sets = !experts ? static_cast<double>((m + p.cols - 1) / p.cols)
+                          : mean > 16 ? a->E * (mean / p.cols + 0.5) : crowds.sets(p.cols);
+      for (p.r = 1; p.r <= (group == 32 ? 1 : 2); ++p.r) {
+        const int parts = w4_parts(p.r, p.nt, group), unit_k = parts * kW4PartK;
+        p.units = (a->K + unit_k - 1) / unit_k;
+        const int64_t blocks = (a->width + per_row * p.r - 1) / (per_row * p.r);
+        const int64_t each = static_cast<int64_t>(ceil(sets * blocks / sms));
+        double rate = p.nt == 2 ? 27 : 41;
+        if (p.r == 2) rate *= 1.08 / (1 + a->K / 18000.);
+        const double item = p.r * p.units * parts / rate;
+        // Column sets that a CTA may meet, and their columns.
+        const int64_t met = sets <= 1 || each == 1 ? 1 : 1 + (each - 1 + blocks - 1) / blocks;
+        const double columns = met * (a->pairs / sets);
+        for (p.team = 1; p.team <= p.warps; p.team *= 2) {
           const int teams = p.warps / p.team;
+          const int64_t rest = each % teams;
           p.rounds = (each + teams - 1) / teams;
-          if (!w4_layout(&p, group, p.rounds, most, experts, a)) continue;
-          const double n = static_cast<double>(each), rounds = static_cast<double>(p.rounds);
-          const double busy = p.warps * n / (rounds * teams);
-          double rate = p.r == 1 ? 27 : p.nt == 1 ? 34 : 30;
-          if (busy < 12) rate *= busy < 8 ? busy / 12 : 0.67 + (busy - 8) / 12;
-          const double chunks = phases == 1 ? 1 : (rounds + a->phase_rounds - 1) / a->phase_rounds;
-          const double time = n * p.r * p.units * parts / rate +
-                              rounds * phases * (p.team == 1 ? 0.2 : 0.3 + 0.05 * p.team) +
-                              chunks * (0.05 * p.cols * a->K / 512 + 1.5 * phases);
+          if (!w4_layout(&p, group, most, experts, a)) continue;
+          if (p.phases == 1) whole = true;
+          double time = (each - rest) * item;
+          if (rest > 0) {
+            const double share = 1.6 * rest * p.team / p.warps;
+            time += rest * item / (share < 1 ? share : 1);
+          }
+          time += p.rounds * p.phases * (p.team == 1 ? 2 : 2.8) +
+                  2.2 * p.phases * (columns <= p.x_cols ? 1 : met) + 0.021 * columns * a->K / 512;
           if (!found || time < least) {
             least = time;
             *best = p;
             found = true;
           }
-          break;
         }
+      }
     }
   }
-  if (found) w4_layout(best, group, best->rounds, most, experts, a);
+  if (found) {
+    a->units = best->units;
+    w4_layout(best, group, most, experts, a);
+  }
   return found;
 }
 
@@ -219,12 +261,14 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.x_cols = p.x_cols;
   a.warps = p.warps;
   a.team = p.team;
-  a.units = p.units;
   a.phase_units = p.phase_units;
   a.wait_limit_ns = kWaitLimitNs;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
   a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
-  int64_t ctas = p.sets * a.row_blocks;
+  // At most as many items: each column set has an expert of its own or is full.
+  int64_t ctas = experts ? E + pairs / p.cols : (pairs + p.cols - 1) / p.cols;
+  if (ctas > pairs) ctas = pairs;
+  ctas *= a.row_blocks;
   if (ctas > d->sms) ctas = d->sms;
   const W4Kernel kern = w4_kernel(scales_type, zeros != nullptr, experts, p.r, p.nt, group);
   return launch_pdl(kern, a, ctas, p.warps * 32, static_cast<size_t>(a.smem_bytes), 1,

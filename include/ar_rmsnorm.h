@@ -465,7 +465,7 @@ int ar_w4_matvec(const void *x, const void *q, const void *scales,
  * ar_w4_matvec with the weights of the routed experts:
  *   out[i, j, :] = x_ij * W[ids[i, j] - first]^T
  * An expert's weights are read once for all its tokens (per 8 of them, or 16
- * where more than six an expert are the rule).  The order of the fp32 sums of
+ * where sixteen an expert are the rule).  The order of the fp32 sums of
  * a row depends on the ids of the batch; equal calls give equal bits.  The
  * pages have no counterpart of it.
  *   x            [m, K] bf16 with x_per_pair = 0 (every choice of a token
