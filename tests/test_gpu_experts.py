@@ -258,6 +258,10 @@ EXPERTS = [
     (5, 6, 2, 512, 64, 128, "bf16", False, "none", False, 1.0),     # nobody here
     (24, 64, 8, 2048, 4096, 128, "bf16", False, "silu_mul", False, 0.0),
     (16, 3, 2, 16384, 40, 64, "bf16", True, "none", True, 0.0),
+    (16, 64, 8, 7168, 40, 128, "bf16", False, "silu_mul", False, 0.0),  # sets of 7, one phase
+    (12, 40, 4, 7040, 34, 64, "f16", True, "none", False, 0.1),         # a part behind the row's end
+    (64, 2, 1, 1152, 2000, 128, "bf16", True, "none", False, 0.0),      # two row and two column tiles
+    (300, 3, 1, 384, 700, 64, "f32", True, "silu_mul", True, 0.0),
 ]
 
 
@@ -324,6 +328,33 @@ def test_w4_matvec_experts_of_a_rank():
         local = torch.where((ids >= first) & (ids < first + count), ids - first, -1).int()
         ref.close(got, *expert_rows(x, local, q[sl], s[sl], z[sl], "none"))
         assert not bool(got[local < 0].any())
+
+
+@pytest.mark.parametrize("m,K,N", [(16, 7168, 24), (9, 1024, 5000)])
+def test_w4_matvec_experts_with_every_token_on_one_expert(m, K, N):
+    """More tokens than a set has columns, all on one expert; the others idle."""
+    g = gen(16)
+    x = normal(g, m, K)
+    q, s, z = weights4(g, (32, N), K, 128, "bf16", False)
+    ids = torch.full((m, 4), 7, device=DEV, dtype=torch.int32)
+    ids[3, 1:] = torch.tensor([0, 31, 32], dtype=torch.int32)
+    ref.close(arn.ar_w4_matvec_experts(x, ids, q, s), *expert_rows(x, ids, q, s, z, "none"))
+
+
+@pytest.mark.parametrize("m", [1, 9])
+@pytest.mark.parametrize("K,group", [(128, 128), (384, 128), (192, 64), (320, 64), (64, 64), (96, 32)])
+def test_w4_scales_behind_a_rows_end_take_no_part(m, K, group):
+    """The next row's NaN scales lie where a row's last, unfinished unit ends."""
+    g = gen(17)
+    x = normal(g, m, K)
+    for kind in ("f32", "bf16", "f16"):
+        for zeros in (False, True):
+            q, s, z = weights4(g, (50,), K, group, kind, zeros)
+            clean = arn.ar_w4_matvec(x, q, s, zeros=z)
+            s2 = s.clone()
+            s2[1::2] = math.nan
+            out = arn.ar_w4_matvec(x, q, s2, zeros=z)
+            assert torch.equal(out[:, ::2], clean[:, ::2]) and bool(out[:, 1::2].isnan().all())
 
 
 def test_w4_nan_and_infinite_rows_stay_their_own():
