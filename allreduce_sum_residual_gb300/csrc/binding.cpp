@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -63,13 +63,14 @@ const void *optional(PyObject *o, at::ScalarType type, at::IntArrayRef shape, in
   return o == Py_None ? nullptr : input(o, type, shape, dev);
 }
 
-// An output: the caller's tensor, or a new one.
+// An output: the caller's tensor, or a new one (straight from the caching
+// allocator: through the dispatcher each takes 0.5 us more).
 struct Output {
   at::Tensor t;
   void *p;
   Output(PyObject *o, at::ScalarType type, at::IntArrayRef shape, const at::Tensor &like, int dev) {
     if (o == Py_None) {
-      t = at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+      t = at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
     } else {
       t = tensor(o);
       want(is_like(t, type, shape, dev));
