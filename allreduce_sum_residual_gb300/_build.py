@@ -58,11 +58,11 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build_binding(force: bool = False):
     """Compile _binding.so unless it is newer than its sources and torch (not
-    without torch: the C library needs none)."""
+    without a CUDA build of torch: the C library needs none)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
+    torch = spec.submodule_search_locations[0] if spec else ""
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
         return None
-    torch = spec.submodule_search_locations[0]
     deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.join(torch, "version.py"),
             os.path.abspath(__file__)]
     if not force and os.path.exists(BINDING) and \
