@@ -138,9 +138,9 @@ struct Crowds {
 //     with two column tiles (16 x 2048 x 32768: 17.4 us, where one reads the
 //     weights twice in 19.9 us).  A last round of few warps is not much
 //     faster than their share.
-//   - The end of a round costs 2 us, with the joined sums of larger teams 2.8
-//     us (1 x 7168 x 7168: 14.4, 11.8, 10.7 and 11.8 us with teams of 1, 2, 4
-//     and 8).
+//   - The end of a round costs 2 us, with the joined sums of larger teams 2.6
+//     to 3.3 us (1 x 7168 x 7168: 14.4, 11.8, 10.7 and 11.8 us with teams of
+//     1, 2, 4 and 8).
 //   - x takes 0.021 us a KB to unpack, and 2.2 us each time.  Experts, which
 //     seldom have all the columns that a set could, take a few less where
 //     that spares the phases (16 tokens of 7168, 8 of 64 experts: 7 columns
@@ -186,7 +186,7 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
             const double share = 1.6 * rest * p.team / p.warps;
             time += rest * item / (share < 1 ? share : 1);
           }
-          time += p.rounds * p.phases * (p.team == 1 ? 2 : 2.8) +
+          time += p.rounds * p.phases * (p.team == 1 ? 2 : 2.5 + 0.05 * p.team) +
                   2.2 * p.phases * (columns <= p.x_cols ? 1 : met) + 0.021 * columns * a->K / 512;
           if (!found || time < least) {
             least = time;
