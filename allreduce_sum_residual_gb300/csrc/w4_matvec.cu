@@ -168,12 +168,13 @@ static bool w4_plan(int64_t m, bool experts, int group, int64_t most, int sms, W
         const int parts = w4_parts(p.r, p.nt, group), unit_k = parts * kW4PartK;
         p.units = (a->K + unit_k - 1) / unit_k;
         const int64_t blocks = (a->width + per_row * p.r - 1) / (per_row * p.r);
-        const int64_t each = static_cast<int64_t>(ceil(sets * blocks / sms));
+        const int64_t each = static_cast<int64_t>(
+            experts ? ceil(sets * blocks / sms) : ceil(blocks / floor(sms / sets)));
         double rate = p.nt == 2 ? 27 : 41;
         if (p.r == 2) rate *= 1.08 / (1 + a->K / 18000.);
         const double item = p.r * p.units * parts / rate;
         // Column sets that a CTA may meet, and their columns.
-        const int64_t met = sets <= 1 || each == 1 ? 1 : 1 + (each - 1 + blocks - 1) / blocks;
+        const int64_t met = !experts || each == 1 ? 1 : 1 + (each - 1 + blocks - 1) / blocks;
         const double columns = met * (a->pairs / sets);
         for (p.team = 1; p.team <= p.warps; p.team *= 2) {
           const int teams = p.warps / p.team;
@@ -265,11 +266,17 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.wait_limit_ns = kWaitLimitNs;
   const int64_t per_block = (act == AR_ACT_SILU_MUL ? 8 : 16) * p.r;
   a.row_blocks = static_cast<int>((width + per_block - 1) / per_block);
-  // At most as many items: each column set has an expert of its own or is full.
-  int64_t ctas = experts ? E + pairs / p.cols : (pairs + p.cols - 1) / p.cols;
-  if (ctas > pairs) ctas = pairs;
-  ctas *= a.row_blocks;
-  if (ctas > d->sms) ctas = d->sms;
+  int64_t ctas;
+  if (experts) {  // at most as many as items: each column set has an expert of its own or is full
+    ctas = E + pairs / p.cols;
+    if (ctas > pairs) ctas = pairs;
+    ctas *= a.row_blocks;
+    if (ctas > d->sms) ctas = d->sms;
+  } else {  // at most eight sets
+    const int64_t sets = (m + p.cols - 1) / p.cols;
+    a.set_ctas = static_cast<int>(d->sms / sets < a.row_blocks ? d->sms / sets : a.row_blocks);
+    ctas = sets * a.set_ctas;
+  }
   const W4Kernel kern = w4_kernel(scales_type, zeros != nullptr, experts, p.r, p.nt, group);
   return launch_pdl(kern, a, ctas, p.warps * 32, static_cast<size_t>(a.smem_bytes), 1,
                     static_cast<cudaStream_t>(stream)) == cudaSuccess
