@@ -87,7 +87,6 @@ struct W4Args {
   int act;
   int units;        // units of a row: ceil(K / (128 parts))
   int row_blocks;   // items of a column set
-  int set_ctas;     // one matrix: CTAs of a column set
   int cols;         // most columns of a set
   int x_cols;       // columns of x that shared memory holds (at least cols)
   int warps, team;  // of a CTA, of a team
@@ -97,6 +96,7 @@ struct W4Args {
   int smem_bytes;
   uint64_t wait_limit_ns;
   int *status;
+  int set_ctas;  // one matrix: CTAs of a column set
 };
 
 constexpr int kW4MaxSets = 32;   // column sets staged at a time
@@ -267,26 +267,22 @@ __device__ __forceinline__ int w4_row(const W4Args &a, int block, int lr) {
   return min(block * 16 * R + lr, a.N - 1);
 }
 
-// Share number i of n of `total` items (at most 4096 sets x 65536 blocks).
-__device__ __forceinline__ void w4_share(unsigned total, unsigned i, unsigned n, int *first,
-                                         int *end) {
-  const unsigned each = total / n, more = total - each * n;
-  *first = static_cast<int>(i * each + min(i, more));
-  *end = *first + static_cast<int>(each + (i < more ? 1u : 0u));
-}
-// This CTA's share: of one column set's items, where the sets are known to
-// the host (none then unpacks the x of two: 16 x 4096 x 4096 in 12 us against
-// 15 us), else of all.
+// This CTA's share of the items (at most 4096 sets x 65536 blocks): of one
+// column set's, where the sets are known to the host (none then unpacks the x
+// of two: 16 x 4096 x 4096 in 12 us against 15 us), else of all.
 template <bool EXPERTS>
 __device__ __forceinline__ void w4_range(const W4Args &a, int nsets, int *first, int *end) {
-  if constexpr (EXPERTS) {
-    w4_share(nsets * a.row_blocks, blockIdx.x, gridDim.x, first, end);
-  } else {
-    const unsigned set = blockIdx.x / a.set_ctas;
-    w4_share(a.row_blocks, blockIdx.x - set * a.set_ctas, a.set_ctas, first, end);
-    *first += set * a.row_blocks;
-    *end += set * a.row_blocks;
+  unsigned total = nsets * a.row_blocks, i = blockIdx.x, n = gridDim.x, before = 0;
+  if constexpr (!EXPERTS) {
+    n = a.set_ctas;
+    before = i / n * a.row_blocks;
+    i %= n;
+    total = a.row_blocks;
   }
+  const unsigned each = total / n;
+  const unsigned more = total - each * n;
+  *first = static_cast<int>(before + i * each + min(i, more));
+  *end = *first + static_cast<int>(each + (i < more ? 1u : 0u));
 }
 
 // A warp's way through its CTA's items [item0, item1): chunk by chunk, in
