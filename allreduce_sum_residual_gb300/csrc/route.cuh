@@ -16,11 +16,11 @@
 // choice and looks at neighbours of that order that are nearer than the error
 // bound.  Where they are all that is near (a few rows in a thousand), the k +
 // 1 sigmoids are computed again in fp64, one a lane, and sorted by those;
-// otherwise (another expert near the last choice; a group border too near to
-// call; softmax scores) the warp does the whole row again, in fp64, or in
-// fp32 where the choices rank as the logits and those are compared as they
-// are.  Neighbours with the same logit and bias are exact ties, which need no
-// second look.
+// otherwise (another expert near the last choice, or equal to it where one
+// of these may have to make way; a group border too near to call; softmax
+// scores) the warp does the whole row again, in fp64, or in fp32 where the
+// choices rank as the logits and those are compared as they are.  Neighbours
+// with the same logit and bias are exact ties, which need no second look.
 //
 // Bound by instructions, some 700 a row of 256 experts: 16384 such rows with
 // groups and bias take 16.2 us (52 us with k passes over every lane's choices
@@ -485,17 +485,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(V))
           const float ck = __shfl_sync(0xFFFFFFFFu, cs, a.k - 1);
           const float xk = __shfl_sync(0xFFFFFFFFu, xs, a.k - 1);
           const float bk = __shfl_sync(0xFFFFFFFFu, bs, a.k - 1);
+          // In the upper half its equals themselves, which matter where one
+          // of the choices before it may belong behind it.
           int rivals = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float c = x[i] > -INFINITY ? quick_score(softmax, x[i], sc.top, inv) + bias[i] : -INFINITY;
-            rivals += kept && i < count && !(c <= ck - delta) && c > -INFINITY &&
-                              !(x[i] == xk && bias[i] == bk)
-                          ? 1 : 0;
+            if (kept && i < count && !(c <= ck - delta) && c > -INFINITY)
+              rivals += x[i] == xk && bias[i] == bk ? 1 << 16 : 1;
           }
-          const uint32_t found = __ballot_sync(
-              0xFFFFFFFFu, lane <= a.k && order > 1u && !(cs <= ck - delta) && !(xs == xk && bs == bk));
-          again |= softmax || static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rivals)) > __popc(found);
+          const int all = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, rivals));
+          const bool known = lane <= a.k && order > 1u && !(cs <= ck - delta);
+          const bool equal = xs == xk && bs == bk;
+          const uint32_t found = __ballot_sync(0xFFFFFFFFu, known && !equal);
+          const uint32_t equals = __ballot_sync(0xFFFFFFFFu, known && equal);
+          const bool behind = __any_sync(0xFFFFFFFFu, known && lane < a.k && !equal && !(cs > ck + delta));
+          again |= softmax || (all & 0xFFFF) > __popc(found) || (behind && all >> 16 > __popc(equals));
           if (near && !again) {
             // These k + 1 in the order of their fp64 choices.
             double exact = -INFINITY;
