@@ -221,6 +221,18 @@ __device__ __noinline__ int order_row_exactly(const RouteArgs &a, const float (&
   return order_row<double, V>(a, x, valid, first, s);
 }
 
+// Weights of a row with a chosen sigmoid score below e^-80, near fp32's end,
+// where its share of the sum may still be any number: in fp64 up to the one
+// rounding.
+static __device__ __noinline__ float far_sigmoid_weight(float x, bool chosen, bool renorm, float scale) {
+  double s = chosen ? score_of<double>(false, x, Scale<double>{0.0, 1.0}) : 0.0;
+  if (renorm) {
+    const double total = warp_total(s);
+    s = total == 0.0 ? 0.0 : s / total;
+  }
+  return static_cast<float>(s * scale);
+}
+
 // A score to a few 2^-24 of 1, in few instructions: ex2.approx is off by 2
 // ulp and its argument by half of one (of x - top or x, whose exponential or
 // derivative makes up for its size), rcp.approx by 1; what they flush to zero
@@ -532,24 +544,29 @@ __global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(V))
       }
     }
     float w = 0.f;
-    if (softmax && a.renorm) {
-      // Relative to the largest chosen logit: the row's sum cancels, and the
-      // chosen cannot all underflow.
-      const float t = warp_max(lane < a.k ? xs : -INFINITY);
-      if (lane < a.k && t > -INFINITY) w = expf(xs - t);
-      bool poison = false;  // a NaN or +inf anywhere in the row makes every score NaN
+    if (!softmax && __any_sync(0xFFFFFFFFu, lane < a.k && xs < -80.f && xs > -INFINITY)) {
+      w = far_sigmoid_weight(xs, lane < a.k, a.renorm != 0, a.scale);
+    } else {
+      if (softmax && a.renorm) {
+        // Relative to the largest chosen logit: the row's sum cancels, and the
+        // chosen cannot all underflow.
+        const float t = warp_max(lane < a.k ? xs : -INFINITY);
+        if (lane < a.k && t > -INFINITY) w = expf(xs - t);
+        bool poison = false;  // a NaN or +inf anywhere in the row makes every score NaN
 #pragma unroll
-      for (int i = 0; i < V; ++i) poison |= i < count && !(x[i] < INFINITY);
-      if (__any_sync(0xFFFFFFFFu, poison)) w = __int_as_float(0x7FC00000);
-    } else if (lane < a.k) {
-      w = sc.sum == 0.f ? 0.f : score_of<float>(softmax, xs, sc);  // 0: a row with nothing on
-    }
-    if (a.renorm) {
-      const float total = warp_total(lane < a.k ? w : 0.f);
-      w = total == 0.f ? 0.f : w / total;
+        for (int i = 0; i < V; ++i) poison |= i < count && !(x[i] < INFINITY);
+        if (__any_sync(0xFFFFFFFFu, poison)) w = __int_as_float(0x7FC00000);
+      } else if (lane < a.k) {
+        w = sc.sum == 0.f ? 0.f : score_of<float>(softmax, xs, sc);  // 0: a row with nothing on
+      }
+      if (a.renorm) {
+        const float total = warp_total(lane < a.k ? w : 0.f);
+        w = total == 0.f ? 0.f : w / total;
+      }
+      w *= a.scale;
     }
     if (lane < a.k) {
-      a.w[row * a.k + lane] = w * a.scale;
+      a.w[row * a.k + lane] = w;
       a.ids[row * a.k + lane] = id;
     }
   }

@@ -406,7 +406,8 @@ int ar_rmsnorm_two_stage_static(const void *const *partials, int n,
  *           experts of the topk_groups best groups can be chosen
  *   ids     the k largest choices, largest first
  *   weights s of the chosen (the bias only steers the choice); with renorm
- *           divided by their sum (0 where that is 0); times `scale`.
+ *           divided by their sum (0 where that is 0); times `scale`.  Sigmoid
+ *           scores below e^-80 count as in 64 bits, where they end at e^-709.
  * Equal choices, and equal groups, go to the lowest index; "equal" and
  * "larger" are decided as 64-bit arithmetic decides them, so ids do not
  * depend on the launch shape.  A logit of -inf is an expert that is off: its

@@ -106,3 +106,42 @@ def test_equals_and_near_softmax_scores():
     w, ids = arn.ar_route_experts(x, 6, **kw)
     rw, rids = ref.route(x, 6, **kw)
     assert torch.equal(ids.cpu(), rids)
+
+
+@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("lo,hi", [(-690, -88), (-200, -90), (-120, -60), (-89, -87), (-500, 3)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_sigmoid_weights_far_below_zero(kind, lo, hi, grouped):
+    """Scores that fp32 cannot hold, whose weights it can: as in 64 bits.  Two
+    roundings (the weight, and nothing before it but fp64): 2^-23, and half of
+    fp32's smallest step."""
+    g = gen(31)
+    x = (torch.rand((40, 64), generator=g, device=DEV) * (hi - lo) + lo).to(TYPES[kind])
+    x[1, 3:] = -math.inf   # fewer on than are chosen
+    x[2] = lo              # equal weights
+    x[3, ::2] = torch.finfo(TYPES[kind]).min
+    kw = dict(groups=8, topk_groups=4, group_score="top2") if grouped else {}
+    for bias in (None, (torch.rand(64, generator=g, device=DEV) - 0.5)):
+        for renorm, scale in ((True, 1.0), (True, 2.5), (False, 1.0), (False, 1e30)):
+            k = dict(bias=bias, scoring="sigmoid", renorm=renorm, scale=scale, **kw)
+            w, ids = arn.ar_route_experts(x, 6, **k)
+            rw, rids = ref.route(x, 6, **k)
+            assert torch.equal(ids.cpu(), rids)
+            # Rows with no score near fp32's end keep its roundings (2^-18).
+            cx = x.gather(1, ids.long()).cpu()
+            far = ((cx < -80) & (cx > -math.inf)).any(1, keepdim=True)
+            tol = torch.where(far, 2.0 ** -23, 2.0 ** -18)
+            err = (w.cpu().double() - rw).abs()
+            assert bool((err <= tol * rw.abs() + 2.0 ** -150).all()), float((err / rw.abs()).nan_to_num().max())
+
+
+def test_sigmoid_weights_where_64_bits_have_none():
+    """Logits of the type's lowest value: a score of 0 in 64 bits too, and
+    weights of 0 where there is nothing else."""
+    for kind in TYPES.values():
+        x = torch.full((2, 16), torch.finfo(kind).min, device=DEV, dtype=kind)
+        x[1, 5] = -600
+        for bias in (None, torch.zeros(16, device=DEV)):
+            w, ids = arn.ar_route_experts(x, 4, bias=bias, scoring="sigmoid")
+            assert ids.tolist() == [[0, 1, 2, 3], [5, 0, 1, 2]]
+            assert w.tolist() == [[0.0] * 4, [1.0, 0.0, 0.0, 0.0]]
