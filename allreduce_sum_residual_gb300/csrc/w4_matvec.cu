@@ -247,7 +247,9 @@ static int run_w4(const void *x, int x_per_pair, const int32_t *ids, int64_t m, 
   a.pairs = static_cast<int>(pairs);
   a.k = x_per_pair ? 1 : k;
   a.first = first;
-  a.E = E;
+  // No int32 behind the largest: an id that wraps around is no expert here.
+  const int64_t numbered = int64_t{INT32_MAX} - first + 1;
+  a.E = static_cast<int>(E < numbered ? E : numbered);
   a.N = static_cast<int>(N);
   a.K = static_cast<int>(K);
   a.ng = static_cast<int>(ng);
