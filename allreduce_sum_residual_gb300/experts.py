@@ -8,6 +8,7 @@ one step; what that does not take (a given stream, another device than the
 current one, anything wrong) goes the long way here, which names what is
 wrong."""
 import ctypes
+import operator
 
 import torch
 
@@ -80,13 +81,29 @@ def _device_of(t, name):
     raise TypeError(f"{name} must be a torch.Tensor")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _whole(value, name):
+    """A whole number for a C int, which ctypes would cut off to 32 bits."""
+    v = operator.index(value)
+    if -_INT_MAX - 1 <= v <= _INT_MAX:
+        return v
+    raise ValueError(f"{name} must be a 32-bit whole number, got {v}")
+
+
+def _size(n):
+    """A tensor's size for a C int: one that does not fit is above every limit."""
+    return n if n <= _INT_MAX else _INT_MAX
+
+
 def _option(table, value, name):
     """An option by its name or its AR_* number (the library checks the number)."""
     if isinstance(value, str):
         if value in table:
             return table[value]
         raise ValueError(f"{name} must be one of {', '.join(sorted(table))}, got {value!r}")
-    return int(value)
+    return _whole(value, name)
 
 
 def _new(like, shape, dtype, stream):
@@ -143,7 +160,11 @@ def ar_route_experts(logits, k, bias=None, scoring="softmax", groups=1, topk_gro
         raise ValueError("the rows of logits must be contiguous")
     if m <= 1:
         row = E
-    k = int(k)
+    k = _whole(k, "k")
+    groups = _whole(groups, "groups")
+    topk_groups = groups if topk_groups is None else _whole(topk_groups, "topk_groups")
+    scoring = _option(SCORES, scoring, "scoring")
+    group_score = _option(GROUP_SCORES, group_score, "group_score")
     shape = (m, k if k > 0 else 0)
     b = None if bias is None else _want(bias, "bias", _F32, (E,), dev)
     if weights is None:
@@ -157,9 +178,7 @@ def ar_route_experts(logits, k, bias=None, scoring="softmax", groups=1, topk_gro
     else:
         i = _want(ids, "ids", _I32, shape, dev)
     _call(_lib().ar_route_experts, "ar_route_experts", dev, stream, logits.data_ptr(), kind, row, b,
-          m, E, k, _option(SCORES, scoring, "scoring"), groups,
-          groups if topk_groups is None else topk_groups,
-          _option(GROUP_SCORES, group_score, "group_score"), 1 if renorm else 0, scale, w, i)
+          m, _size(E), k, scoring, groups, topk_groups, group_score, 1 if renorm else 0, scale, w, i)
     return weights, ids
 
 
@@ -185,7 +204,7 @@ def _w4_operands(q, scales, zeros, K, lead, dev):
     qa = _want(q, "q", _U8, of_q, dev)
     sa = _want(scales, "scales", scales.dtype, shape, dev)
     za = None if zeros is None else _want(zeros, "zeros", _U8, shape, dev)
-    return of_q[-2], K // ng, qa, sa, kind, za
+    return of_q[-2], _size(K // ng), qa, sa, kind, za
 
 
 def ar_w4_matvec(x, q, scales, zeros=None, act="none", out=None, stream=None):
@@ -241,7 +260,7 @@ def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", first=0, out
     K = of_x[-1]
     xa = _want(x, "x", _BF16, (m, k, K) if per_pair else (m, K), dev)
     N, group, qa, sa, kind, za = _w4_operands(q, scales, zeros, K, 1, dev)
-    act = _option(ACTS, act, "act")
+    act, first = _option(ACTS, act, "act"), _whole(first, "first")
     shape = (m, k, N // 2 if act == AR_ACT_SILU_MUL else N)
     if out is None:
         out = _new(x, shape, _BF16, stream)
@@ -249,7 +268,8 @@ def ar_w4_matvec_experts(x, ids, q, scales, zeros=None, act="none", first=0, out
     else:
         oa = _want(out, "out", _BF16, shape, dev)
     _call(_lib().ar_w4_matvec_experts, "ar_w4_matvec_experts", dev, stream, xa,
-          1 if per_pair else 0, ia, m, k, qa, sa, kind, za, first, q.shape[0], N, K, group, act, oa)
+          1 if per_pair else 0, ia, m, _size(k), qa, sa, kind, za, first, _size(q.shape[0]), N, K,
+          group, act, oa)
     return out
 
 
@@ -295,7 +315,7 @@ def ar_combine(y, weights, shared=None, slots=None, out=None, stream=None):
         oa = out.data_ptr()
     else:
         oa = _want(out, "out", _BF16, shape, dev)
-    _call(_lib().ar_combine, "ar_combine", dev, stream, ya, rows, sa, wa, ha, m, k, H, oa)
+    _call(_lib().ar_combine, "ar_combine", dev, stream, ya, rows, sa, wa, ha, m, _size(k), H, oa)
     return out
 
 
@@ -324,5 +344,5 @@ def ar_combine_rmsnorm(y, weights, residual, weight, eps, shared=None, slots=Non
     else:
         oo = _want(residual_out, "residual_out", _BF16, shape, dev)
     _call(_lib().ar_combine_rmsnorm, "ar_combine_rmsnorm", dev, stream, ya, rows, sa, wa, ha, ra, ga,
-          eps, m, k, H, oa, oo)
+          eps, m, _size(k), H, oa, oo)
     return out, residual_out
