@@ -285,6 +285,84 @@ __device__ __forceinline__ void w4_range(const W4Args &a, int nsets, int *first,
   *end = *first + static_cast<int>(each + (i < more ? 1u : 0u));
 }
 
+// One output, by one thread: x as it is, a group's products in fp32, times
+// its scale.
+template <int ST, bool ZEROS>
+__device__ float w4_dot(const W4Args &a, const uint4 *x, int64_t row) {
+  const int eights = a.K / a.ng / 8;  // of a group
+  const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row * (a.K / 2));
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < a.ng; ++i) {
+    const int64_t el = row * a.ng + i;
+    const float s =
+        ST == AR_TYPE_F32
+            ? __ldg(reinterpret_cast<const float *>(a.scales) + el)
+            : __uint_as_float(uint32_t{__ldg(reinterpret_cast<const uint16_t *>(a.scales) + el)} << 16);
+    const float z = ZEROS ? static_cast<float>(__ldg(a.zeros + el) & 15) : 8.f;
+    float d = 0.f;
+#pragma unroll 1
+    for (int k8 = i * eights; k8 < (i + 1) * eights; ++k8) {
+      const uint32_t word = __ldg(q + k8);
+      float v[8];
+      unpack8(__ldg(x + k8), v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d = fmaf(static_cast<float>(word >> 4 * j & 15u) - z, v[j], d);
+    }
+    sum = fmaf(s, d, sum);
+  }
+  return sum;
+}
+
+// This CTA's outputs that are no finite numbers, again.
+// A scale of 2^95 or more times a sum of x as fp16 can pass fp32's end where
+// the column's power of two would have brought the result back.  (bf16 and
+// fp32 scales; 2^16 is fp16's largest.)  Behind the items, where it takes none
+// of their registers: the power of two of each product in front of its scale
+// cost 2 to 8 % of every call, a second look at each item's sums 4 %.
+template <int R, int ST, bool ZEROS, bool EXPERTS>
+__device__ __noinline__ void w4_again(const W4Args &a, const int *sets, const int16_t *ids16,
+                                      int *col_pair) {
+  const int lane = threadIdx.x & 31, threads = blockDim.x;
+  int item0, item1;
+  w4_range<EXPERTS>(a, EXPERTS ? sets[a.E] : 0, &item0, &item1);
+  const int outs = a.act == AR_ACT_SILU_MUL ? 8 * R : 16 * R;
+  int e = 0;
+  for (int item = item0; item < item1; ++item) {
+    const int set = item / a.row_blocks, block = item - set * a.row_blocks;
+    if constexpr (EXPERTS)
+      while (sets[e + 1] <= set) ++e;
+    const int skip = (EXPERTS ? set - sets[e] : set) * a.cols;
+    if (item == item0 || block == 0) {  // the set's pairs, in order
+      __syncthreads();
+      if (threadIdx.x < 32) {
+        int seen = 0;
+        for (int p0 = 0; p0 < a.pairs; p0 += 32) {
+          const bool is = p0 + lane < a.pairs && (!EXPERTS || ids16[p0 + lane] == e);
+          const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
+          const int k = seen + __popc(who & ((1u << lane) - 1u)) - skip;
+          if (is && k >= 0 && k < a.cols) col_pair[k] = p0 + lane;
+          seen += __popc(who);
+        }
+        if (lane == 0) col_pair[kW4MaxXCols - 1] = min(a.cols, seen - skip);
+      }
+      __syncthreads();
+    }
+    const int n = col_pair[kW4MaxXCols - 1];
+    for (int i = threadIdx.x; i < n * outs; i += threads) {
+      const int col = i / outs, row = block * outs + i % outs, pair = col_pair[col];
+      if (row >= a.width) continue;
+      __nv_bfloat16 *to = a.out + static_cast<int64_t>(pair) * a.width + row;
+      if (fabsf(__bfloat162float(*to)) < INFINITY) continue;
+      const uint4 *x = a.x + static_cast<int64_t>(pair / a.k) * (a.K / 8);
+      const int64_t at = static_cast<int64_t>(e) * a.N + row;
+      float v = w4_dot<ST, ZEROS>(a, x, at);
+      if (a.act == AR_ACT_SILU_MUL) v = gated(v, w4_dot<ST, ZEROS>(a, x, at + a.width));
+      if (v == v) *to = __float2bfloat16_rn(v);  // x next to its largest may give inf - inf here alone
+    }
+  }
+}
+
 // A warp's way through its CTA's items [item0, item1): chunk by chunk, in
 // each chunk phase by phase, in each phase the team's items, and of all their
 // units in a row every team'th.  One phase: one chunk.
@@ -386,6 +464,8 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   // Of team and buffer: all warps have left their sums, all have read them.
   __shared__ uint64_t full[kW4MaxWarps], empty[kW4MaxWarps];
   __shared__ int aborted;
+  __shared__ bool col_odd[kW4MaxXCols];  // whether a column has an infinity or a NaN
+  __shared__ bool again;                 // some output of another is no finite number
 
   int nsets = (a.pairs + a.cols - 1) / a.cols;
   if constexpr (!EXPERTS) {
@@ -411,7 +491,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     mbar_init(&empty[tid], a.team);
   }
   if (tid < 20) nothing[tid] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) aborted = 0;
+  if (tid == 0) aborted = 0, again = false;
   if constexpr (EXPERTS) {
     for (int e = tid; e <= AR_MAX_EXPERTS; e += threads) sets[e] = 0;
     __syncthreads();
@@ -628,7 +708,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       }
       uint32_t top = max(tops & 0xFFFFu, tops >> 16);
       if (top >= 0x7F80u) {  // an infinity or a NaN: the largest of the others
-        top = 0;
+        top = 0, col_odd[col] = true;
         for (int j = j0; j < whole; j += step) {
           const uint4 v = __ldg(row + j);
           const uint32_t e[4] = {v.x, v.y, v.z, v.w};
@@ -660,6 +740,13 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     __syncthreads();
   };
 
+  // fp16 scales cannot pass fp32's end.
+  auto put = [&](__nv_bfloat16 *to, float v, int col) {
+    *to = __float2bfloat16_rn(v);
+    if constexpr (ST != AR_TYPE_F16)
+      if (!(fabsf(v) < INFINITY) && !col_odd[col]) again = true;
+  };
+
   int done = 0;  // items of this team that its warps have left (its buffers' phases)
   struct Item {
     int block, col, ncols, round;
@@ -688,7 +775,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       }
       const int n0 = it.block * outs + o;
       if (last && n0 < a.width)
-        a.out[static_cast<int64_t>(col_pair[it.col + col]) * a.width + n0] = __float2bfloat16_rn(v);
+        put(a.out + static_cast<int64_t>(col_pair[it.col + col]) * a.width + n0, v, it.col + col);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[at]);
@@ -734,7 +821,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
           if (fit >> lane & 1u) set_col[lane + 1] = before;
         }
         for (int c = tid; c < kW4MaxXCols; c += threads) {
-          col_top[c] = 0;
+          col_top[c] = 0, col_odd[c] = false;
           if constexpr (!EXPERTS) col_pair[c] = set0 * a.cols + c;  // the sets are full but the last
         }
         __syncthreads();
@@ -902,10 +989,10 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
                 if (!last) continue;
                 if (act) {  // R = 1: gate and up rows eight apart, R = 2: sixteen
                   if constexpr (R == 1) {
-                    if (o0 < a.width) to[0] = __float2bfloat16_rn(gated(v[0][0], v[0][1]));
+                    if (o0 < a.width) put(to, gated(v[0][0], v[0][1]), it.col + col);
                   } else {
-                    if (o0 < a.width) to[0] = __float2bfloat16_rn(gated(v[0][0], v[1][0]));
-                    if (o0 + 8 < a.width) to[8] = __float2bfloat16_rn(gated(v[0][1], v[1][1]));
+                    if (o0 < a.width) put(to, gated(v[0][0], v[1][0]), it.col + col);
+                    if (o0 + 8 < a.width) put(to + 8, gated(v[0][1], v[1][1]), it.col + col);
                   }
                 } else {
 #pragma unroll
@@ -913,7 +1000,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                       if (o0 + r * 16 + h * 8 < a.width)
-                        to[r * 16 + h * 8] = __float2bfloat16_rn(v[r][h]);
+                        put(to + r * 16 + h * 8, v[r][h], it.col + col);
                 }
               }
             continue;
@@ -950,6 +1037,10 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
     base = chunk;
   }
   cp_async_wait<0>();
+  if constexpr (ST != AR_TYPE_F16) {
+    __syncthreads();
+    if (again) w4_again<R, ST, ZEROS, EXPERTS>(a, sets, ids16, col_pair);
+  }
 }
 
 using W4Kernel = void (*)(W4Args);

@@ -441,9 +441,11 @@ int ar_route_experts(const void *logits, int logits_type, int64_t row_stride,
  * Products are summed in fp32; s multiplies the fp32 sum of its group; one
  * rounding, at the end.  x enters the products as fp16 times a power of two
  * of its row: exact down to 2^-30 of the row's largest finite magnitude,
- * smaller ones to within 2^-38 of it.  The order of the fp32 sums depends on
- * the shape and the device, not on the data, so equal calls give equal bits,
- * and a row of another batch the same up to fp32 rounding.  The pages have no
+ * smaller ones to within 2^-38 of it.  A result is infinite only where sums of
+ * its own size pass fp32's end, whatever the sizes of x and s.  The order of
+ * the fp32 sums depends on the shape and the device, and where they passed
+ * fp32's end on the way on the data too; equal calls give equal bits, and a
+ * row of another batch the same up to fp32 rounding.  The pages have no
  * counterpart of it.
  *   x        [m, K] bf16.  m <= AR_MATVEC_MAX_ROWS.
  *   q        [N, K/2] bytes, two weights each: the low four bits hold the
