@@ -3,8 +3,9 @@
 Each .cu file compiles to an object in parallel; the objects link into
 ``allreduce_sum_residual_gb300/libarnorm.so``.  Only nvcc is needed (no
 cmake); the same command works on x86_64 and aarch64 hosts.  Beside it g++
-builds ``_binding.so``, the expert-layer calls on torch tensors, against the
-installed torch.
+builds ``_binding.so``, the expert-layer calls on torch tensors in one step,
+against the installed torch; where that cannot be built
+the library stands alone and those calls go through ctypes.
 """
 import concurrent.futures as cf
 import glob
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +27,8 @@ LIB = os.path.join(PKG, "libarnorm.so")
 # device status word and skips the access.  For tests, not for production.
 CHECK_OBJ_DIR = os.path.join(PKG, "_build_check")
 CHECK_LIB = os.path.join(PKG, "libarnorm_check.so")
-BINDING = os.path.join(PKG, "_binding.so")
+CXX = "g++"
+BINDING_DIR = PKG
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -56,21 +59,26 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def binding_path() -> str:
+    return os.path.join(BINDING_DIR, "_binding.so")
+
+
 def build_binding(force: bool = False):
-    """Compile _binding.so unless it is newer than its sources and torch (not
-    without a CUDA build of torch: the C library needs none)."""
+    """Compile the binding unless it is newer than its sources and torch; returns
+    its path, or None without a CUDA build of torch (the C library needs none)."""
     spec = importlib.util.find_spec("torch")
     torch = spec.submodule_search_locations[0] if spec else ""
     if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
         return None
+    path = binding_path()
     deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.join(torch, "version.py"),
             os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+    if not force and os.path.exists(path) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-I{INCLUDE}",
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [CXX, "-std=c++17", "-O2", "-fPIC", "-shared", f"-I{INCLUDE}",
            f"-I{sysconfig.get_paths()['include']}", "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
@@ -78,20 +86,31 @@ def build_binding(force: bool = False):
            "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+        raise RuntimeError(f"{CXX} failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
+def _binding_if_possible(force: bool = False):
+    """build_binding, which the library does not need: a warning where it
+    fails (no g++, no Python.h, no torch headers)."""
+    try:
+        return build_binding(force)
+    except (RuntimeError, OSError) as e:
+        warnings.warn("the expert-layer calls will go through ctypes, some 10 us a call slower: their "
+                      f"binding was not built ({e})", RuntimeWarning, stacklevel=3)
+        return None
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), check: bool = False) -> str:
     """Compile and link libarnorm.so (with ``check``: libarnorm_check.so, the
     checking build) unless it is newer than every source; without ``check``
-    _binding.so too."""
+    the binding too, if it can be built."""
     lib_path, obj_dir = (CHECK_LIB, CHECK_OBJ_DIR) if check else (LIB, OBJ_DIR)
     extra_flags = tuple(extra_flags) + (("-DAR_CHECK=1",) if check else ())
     if not force and up_to_date(lib_path):
         if not check:
-            build_binding()
+            _binding_if_possible()
         return lib_path
     os.makedirs(obj_dir, exist_ok=True)
     cc = nvcc()
@@ -108,7 +127,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), check: boo
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = None if check else ex.submit(build_binding, force)
+        binding = None if check else ex.submit(_binding_if_possible, force)
         objs = list(ex.map(compile_one, srcs))
     tmp = lib_path + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)

@@ -3,12 +3,15 @@ with 4-bit weights, the weighted sum of the experts' outputs.
 
 Argument marshalling only, as in the package itself, which these functions
 are called through (``arn.ar_route_experts`` and so on).  A call on the
-current stream goes through _binding.so, which checks, allocates and calls in
-one step; what that does not take (a given stream, another device than the
-current one, anything wrong) goes the long way here, which names what is
-wrong."""
+current stream goes through the binding (csrc/binding.cpp), which checks,
+allocates and calls in one step; what that does not take (a given stream,
+another device than the current one, anything wrong) goes the long way here,
+which names what is wrong, and so does everything where the binding is not
+built."""
 import ctypes
+import importlib.util
 import operator
+import warnings
 
 import torch
 
@@ -21,22 +24,38 @@ _I32, _U8 = torch.int32, torch.uint8
 _empty = torch.empty
 _raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-_native = None     # _binding.so
+_native = None     # the binding
 _bound_to = None   # the library whose entry points it has
 
 
+class _LongWay:
+    """In the binding's place where there is none."""
+    route_experts = w4_matvec = w4_matvec_experts = combine = combine_rmsnorm = bind = \
+        staticmethod(lambda *_: None)
+
+
+def _load_native():
+    from . import _build
+    path = _build.binding_path()
+    try:
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        warnings.warn("the expert-layer calls go through ctypes, some 10 us a call slower: build their "
+                      "binding with `python -c \"import __graft_entry__ as g; g.build()\"` "
+                      f"({e})", RuntimeWarning, stacklevel=4)
+        return _LongWay
+
+
 def _fast():
-    """_binding.so, with the entry points of the loaded library."""
+    """The binding, with the entry points of the loaded library."""
     global _native, _bound_to
     lib = _lib()
     if lib is not _bound_to:
         if _native is None:
-            try:
-                from . import _binding
-            except ImportError as e:
-                raise RuntimeError("_binding.so is not built: run `python -c \"import __graft_entry__ "
-                                   "as g; g.build()\"` (there is no fallback)") from e
-            _native = _binding
+            _native = _load_native()
         _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                        (lib.ar_route_experts, lib.ar_w4_matvec, lib.ar_w4_matvec_experts,
                         lib.ar_combine, lib.ar_combine_rmsnorm)))
