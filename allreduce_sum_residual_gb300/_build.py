@@ -3,14 +3,15 @@
 Each .cu file compiles to an object in parallel; the objects link into
 ``allreduce_sum_residual_gb300/libarnorm.so``.  Only nvcc is needed (no
 cmake); the same command works on x86_64 and aarch64 hosts.  Beside it g++
-builds ``_binding.so``, the expert-layer calls on torch tensors in one step,
-against the installed torch; where that cannot be built
+builds ``_binding-<python>-<torch>.so``, the expert-layer calls on torch
+tensors in one step, against the installed torch; where that cannot be built
 the library stands alone and those calls go through ctypes.
 """
 import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -59,20 +60,24 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def binding_path() -> str:
-    return os.path.join(BINDING_DIR, "_binding.so")
+def binding_path(torch_version: str, torch_git: str) -> str:
+    """The binding for this Python and that torch, whose internals it calls:
+    another of either neither loads it nor takes it for up to date."""
+    python = sysconfig.get_config_var("EXT_SUFFIX")[1:-len(".so")]
+    return os.path.join(BINDING_DIR, f"_binding-{python}-torch{torch_version}-{torch_git[:9]}.so")
 
 
 def build_binding(force: bool = False):
-    """Compile the binding unless it is newer than its sources and torch; returns
-    its path, or None without a CUDA build of torch (the C library needs none)."""
+    """Compile the binding unless it is newer than its sources; returns its
+    path, or None without a CUDA build of torch (the C library needs none)."""
     spec = importlib.util.find_spec("torch")
     torch = spec.submodule_search_locations[0] if spec else ""
     if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
         return None
-    path = binding_path()
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.join(torch, "version.py"),
-            os.path.abspath(__file__)]
+    with open(os.path.join(torch, "version.py")) as f:
+        said = dict(re.findall(r"^(\w+)\s*(?::[^=]*)?=\s*'([^']*)'", f.read(), re.M))
+    path = binding_path(said["__version__"], said.get("git_version", ""))
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "ar_rmsnorm.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(path) and \
             all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
         return path
@@ -96,7 +101,7 @@ def _binding_if_possible(force: bool = False):
     fails (no g++, no Python.h, no torch headers)."""
     try:
         return build_binding(force)
-    except (RuntimeError, OSError) as e:
+    except (RuntimeError, OSError, KeyError) as e:
         warnings.warn("the expert-layer calls will go through ctypes, some 10 us a call slower: their "
                       f"binding was not built ({e})", RuntimeWarning, stacklevel=3)
         return None

@@ -29,14 +29,14 @@ _bound_to = None   # the library whose entry points it has
 
 
 class _LongWay:
-    """In the binding's place where there is none."""
+    """In the binding's place where there is none for this Python and torch."""
     route_experts = w4_matvec = w4_matvec_experts = combine = combine_rmsnorm = bind = \
         staticmethod(lambda *_: None)
 
 
 def _load_native():
     from . import _build
-    path = _build.binding_path()
+    path = _build.binding_path(torch.__version__, torch.version.git_version or "")
     try:
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
         module = importlib.util.module_from_spec(spec)

@@ -72,3 +72,36 @@ def test_results_without_a_binding_are_the_same(arlib, tmp_path, monkeypatch):
     for name in calls:
         for a, b in zip(want[name], got[name]):
             assert torch.equal(a, b), name
+
+
+@needs_cuda_torch
+def test_another_python_or_torch_has_a_binding_of_its_own(arlib, monkeypatch):
+    """However old its files are: what is compiled against this torch's
+    internals is never loaded with another's."""
+    import sysconfig
+    path = _build.build_binding()
+    git = torch.version.git_version or ""
+    assert path == _build.binding_path(torch.__version__, git) and os.path.exists(path)
+    others = {_build.binding_path("0.0.0+other", git), _build.binding_path(torch.__version__, "0" * 40)}
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda _: ".cpython-000-other.so")
+    others.add(_build.binding_path(torch.__version__, git))
+    assert len(others) == 3 and path not in others
+    assert all(os.path.dirname(p) == _build.BINDING_DIR and p.endswith(".so") for p in others)
+
+
+@needs_cuda_torch
+def test_the_binding_of_another_torch_is_not_loaded(arlib, tmp_path, monkeypatch):
+    import shutil
+    from allreduce_sum_residual_gb300 import experts
+    mine = _build.build_binding()
+    monkeypatch.setattr(_build, "BINDING_DIR", str(tmp_path))
+    monkeypatch.setattr(experts, "_native", None)
+    monkeypatch.setattr(experts, "_bound_to", None)
+    shutil.copy(mine, _build.binding_path("0.0.0+other", torch.version.git_version or ""))
+    shutil.copy(mine, tmp_path / "_binding.so")  # a name without either
+    with pytest.warns(RuntimeWarning, match="ctypes"):
+        assert experts._fast() is experts._LongWay
+    shutil.copy(mine, tmp_path)
+    monkeypatch.setattr(experts, "_native", None)
+    monkeypatch.setattr(experts, "_bound_to", None)
+    assert experts._fast() is not experts._LongWay
