@@ -19,13 +19,15 @@ from .experts import (ar_combine, ar_combine_rmsnorm, ar_route_experts, ar_w4_ma
 class ExpertLayer:
     """The weights of one layer on one rank.
 
-    router: [experts of the layer, H] bf16.  up: (q, scales, zeros or None)
-    of this rank's experts' gate and up rows, [E, 2 I, H] unpacked; down:
-    the same of [E, H, I].  Layouts as in ``ar_w4_matvec``.  first: the
-    layer's number of this rank's first expert.  shared_up, shared_down: a
-    dense expert that every token takes, or None (with a group: this rank's
-    slice of it).  group: a ``peers.FusedAllReduceRMSNorm``, or None for one
-    rank.  The routing options are ``ar_route_experts``'s.
+    router: [experts of the layer, H] bf16 or fp32; its logits are fp32 either
+    way (bf16's rounding would decide between experts).  up: (q, scales,
+    zeros or None) of this rank's experts' gate and up rows, [E, 2 I, H]
+    unpacked; down: the same of [E, H, I].  Layouts as in ``ar_w4_matvec``.
+    first: the layer's number of this rank's first expert.  shared_up,
+    shared_down: a dense expert that every token takes, or None (with a
+    group: this rank's slice of it).  group: a
+    ``peers.FusedAllReduceRMSNorm``, or None for one rank.  The routing
+    options are ``ar_route_experts``'s.
     """
 
     def __init__(self, router, up, down, top_k, *, bias=None, scoring="softmax", groups=1,
@@ -35,10 +37,12 @@ class ExpertLayer:
             raise ValueError("a shared expert needs both shared_up and shared_down")
         if router.dim() != 2:
             raise ValueError("router must be [experts, H]")
+        if router.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"router must be bfloat16 or float32, got {router.dtype}")
         if not 0 <= first <= router.shape[0] - up[0].shape[0]:
             raise ValueError(f"experts {first} .. {first + up[0].shape[0] - 1} are not all among the "
                              f"router's {router.shape[0]}")
-        self.router, self.up, self.down = router, tuple(up), tuple(down)
+        self.router, self.up, self.down = router.detach(), tuple(up), tuple(down)
         self.top_k, self.first, self.group = top_k, first, group
         self.shared_up, self.shared_down = shared_up, shared_down
         self.routing = dict(bias=bias, scoring=scoring, groups=groups, topk_groups=topk_groups,
@@ -46,7 +50,11 @@ class ExpertLayer:
 
     def route(self, x):
         """(weights, ids) of the tokens x [m, H]."""
-        return ar_route_experts(torch.matmul(x, self.router.t()), self.top_k, **self.routing)
+        if self.router.dtype is torch.bfloat16:
+            logits = torch.mm(x, self.router.t(), out_dtype=torch.float32)
+        else:
+            logits = torch.mm(x.float(), self.router.t())
+        return ar_route_experts(logits, self.top_k, **self.routing)
 
     def outputs(self, x):
         """(y, weights, shared): the chosen experts' rows [m, k, H] (zero where

@@ -116,3 +116,51 @@ def test_a_layer_and_its_ranks_against_64_bits(m, case, with_shared):
     ref.close(rout4, r, err4)
     ref.close(out4, *ref.norm(r, err4, gain, 1e-6))
     assert bool(((rout4.double() - rout.double()).abs() <= err + err4 + 2 * ref.BF16 * r.abs()).all())
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_logits_keep_what_bf16_would_lose(kind):
+    """Experts whose logits differ by less than bf16 resolves: the larger one
+    is chosen, also where it has the higher index."""
+    from allreduce_sum_residual_gb300.moe import ExpertLayer
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    w, _, _ = weights(g, False)
+    x = torch.zeros((E - 1, H), dtype=torch.bfloat16, device=DEV)
+    x[:, 0], x[:, 1] = 64, 2.0 ** -4
+    router = torch.zeros((E, H), dtype=kind, device=DEV)
+    router[:, 0] = 1                       # logits of 64 ...
+    router[:, 1] = torch.arange(E, device=DEV) / 16   # ... and up to 2^-4 more
+    layer = ExpertLayer(router, w["up"], w["down"], K)
+    _, ids = layer.route(x)
+    assert ids.tolist() == [[E - 1, E - 2, E - 3]] * (E - 1)
+
+
+def test_an_fp32_router_and_parameters():
+    """A router in fp32 is used as it is; parameters and inputs that autograd
+    follows are read like others; no token at all."""
+    from allreduce_sum_residual_gb300.moe import ExpertLayer
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    w, _, _ = weights(g, False)
+    x = torch.randn((9, H), generator=g, device=DEV).bfloat16()
+    residual, gain = x.roll(1, 0).contiguous(), x[0].clone()
+    want = ExpertLayer(**w, top_k=K)(x, residual, gain, 1e-6)
+    fine = torch.randn((E, H), generator=g, device=DEV) * 0.05
+    weights32, ids = ExpertLayer(fine, w["up"], w["down"], K).route(x)
+    rw, rids = ref.route(x.double() @ fine.double().T, K)
+    assert torch.equal(ids.cpu(), rids) and bool(((weights32.cpu() - rw).abs() <= 1e-5).all())
+    for router in (w["router"], w["router"].float()):
+        layer = ExpertLayer(torch.nn.Parameter(router), w["up"], w["down"], K)
+        xg = x.clone().requires_grad_(True)
+        got = layer(xg, residual, gain, 1e-6)
+        if router is w["router"]:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # fp32 products add up in another order: 512 terms, each way off by 512 2^-24 of
+        # sum |x router| < 128, so weights by less than 2^-7.
+        (wa, ia), (wb, ib) = layer.route(xg), ExpertLayer(**w, top_k=K).route(x)
+        assert torch.equal(ia, ib) and bool(((wa - wb).abs() <= 2.0 ** -7).all())
+        none = layer(x[:0], residual[:0], gain, 1e-6)
+        assert [t.shape for t in none] == [(0, H), (0, H)]
+    with pytest.raises(ValueError, match="router must be"):
+        ExpertLayer(w["router"].half(), w["up"], w["down"], K)
