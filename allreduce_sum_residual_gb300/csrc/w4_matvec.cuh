@@ -545,17 +545,30 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   }
   int item0, item1;
   w4_range<EXPERTS>(a, nsets, &item0, &item1);
-  // Checking build: the launch has the plan's warps and shared memory, whole
-  // teams, and room for a column set.
+  // Checking build: the launch has the plan's warps, whole teams, room for a
+  // column set, and the regions of shared memory that the kernel walks, one
+  // behind the other.
   uint32_t dynamic_bytes;
   asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dynamic_bytes));
-  if (!in_bounds(threads == static_cast<int>(blockDim.x) && warps <= kW4MaxWarps &&
-                     warps % a.team == 0 && a.cols <= 8 * NT && a.cols <= a.x_cols &&
-                     a.x_cols <= kW4MaxXCols &&
-                     static_cast<uint32_t>(a.smem_bytes) <= dynamic_bytes &&
-                     static_cast<int64_t>(nsets) * a.cols >= 0,
-                 a.status))
+  const int tile_bytes = tile * static_cast<int>(sizeof(float));
+  if (!in_bounds(
+          threads == static_cast<int>(blockDim.x) && warps <= kW4MaxWarps && warps % a.team == 0 &&
+              a.cols <= 8 * NT && a.cols <= a.x_cols && a.x_cols <= kW4MaxXCols &&
+              warps * kDepth * kSlot <= a.xs_offset &&
+              a.xs_offset + a.x_cols * min(a.phase_units, a.units) * kParts * 256 <= a.red_offset &&
+              a.red_offset + (a.team > 1 ? 2 * warps * tile_bytes : 0) <= a.acc_offset &&
+              a.acc_offset + (a.phase_units < a.units ? a.phase_rounds * teams * tile_bytes : 0) <=
+                  a.ids_offset &&
+              a.ids_offset + (EXPERTS ? 2 * a.pairs : 0) <= a.smem_bytes &&
+              static_cast<uint32_t>(a.smem_bytes) <= dynamic_bytes &&
+              (!EXPERTS || (nsets >= 0 && nsets <= a.E + a.pairs / a.cols)),
+          a.status))
     item1 = item0;
+  // Checking build: a row of out.
+  auto pair_of = [&](int col) -> int {
+    const int p = col_pair[col];
+    return in_bounds(p >= 0 && p < a.pairs, a.status) ? p : 0;
+  };
 
   // The expert of a column set.
   auto expert_of = [&](int set) -> int {
@@ -684,7 +697,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       return xs + ((j >> 4) * a.x_cols + col) * 16 + (to ^ ((col & 1) << 2));
     };
     for (int col = warp / share; col < n; col += warps / share) {
-      const uint4 *row = a.x + static_cast<int64_t>(col_pair[col] / a.k) * (a.K / 8) + before;
+      const uint4 *row = a.x + static_cast<int64_t>(pair_of(col) / a.k) * (a.K / 8) + before;
       const int whole = min(pieces, a.K / 8 - before);  // eights that the row has here
       uint32_t tops = 0;  // the largest magnitudes of the even and of the odd elements
       for (int j = j0; j < pieces; j += 8 * step) {
@@ -775,7 +788,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
       }
       const int n0 = it.block * outs + o;
       if (last && n0 < a.width)
-        put(a.out + static_cast<int64_t>(col_pair[it.col + col]) * a.width + n0, v, it.col + col);
+        put(a.out + static_cast<int64_t>(pair_of(it.col + col)) * a.width + n0, v, it.col + col);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[at]);
@@ -842,6 +855,14 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
           }
           __syncthreads();
         }
+        // Checking build: the staged sets and their columns have room, and the
+        // rounds of a phase sums of their own.
+        if (!in_bounds(count >= 1 && count <= kW4MaxSets && set_col[count] <= a.x_cols &&
+                           (u1 - u0) <= a.phase_units &&
+                           (a.phase_units >= a.units ||
+                            (end - base + teams - 1) / teams <= a.phase_rounds),
+                       a.status))
+          break;  // the same in every thread
         stage(u0, u1, set_col[count]);
 
 #pragma unroll 1
@@ -975,7 +996,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
                 const int col = n * 8 + 2 * t + c;
                 if (col >= it.ncols) continue;
                 const int o0 = it.block * outs + g;
-                __nv_bfloat16 *to = a.out + static_cast<int64_t>(col_pair[it.col + col]) * a.width + o0;
+                __nv_bfloat16 *to = a.out + static_cast<int64_t>(pair_of(it.col + col)) * a.width + o0;
                 float v[R][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r)
