@@ -42,6 +42,8 @@ class ExpertLayer:
         if not 0 <= first <= router.shape[0] - up[0].shape[0]:
             raise ValueError(f"experts {first} .. {first + up[0].shape[0] - 1} are not all among the "
                              f"router's {router.shape[0]}")
+        if down[0].shape[0] != up[0].shape[0]:
+            raise ValueError(f"up holds {up[0].shape[0]} experts and down {down[0].shape[0]}")
         self.router, self.up, self.down = router.detach(), tuple(up), tuple(down)
         self.top_k, self.first, self.group = top_k, first, group
         self.shared_up, self.shared_down = shared_up, shared_down
