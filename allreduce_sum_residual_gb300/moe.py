@@ -55,7 +55,8 @@ class ExpertLayer:
         if self.router.dtype is torch.bfloat16:
             logits = torch.mm(x, self.router.t(), out_dtype=torch.float32)
         else:
-            logits = torch.mm(x.float(), self.router.t())
+            with torch.autocast("cuda", enabled=False):
+                logits = torch.mm(x.float(), self.router.t())
         return ar_route_experts(logits, self.top_k, **self.routing)
 
     def outputs(self, x):

@@ -164,3 +164,18 @@ def test_an_fp32_router_and_parameters():
         assert [t.shape for t in none] == [(0, H), (0, H)]
     with pytest.raises(ValueError, match="router must be"):
         ExpertLayer(w["router"].half(), w["up"], w["down"], K)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_autocast_leaves_the_logits_alone(kind):
+    from allreduce_sum_residual_gb300.moe import ExpertLayer
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    w, _, _ = weights(g, False)
+    layer = ExpertLayer(w["router"].to(kind), w["up"], w["down"], K)
+    x = torch.randn((33, H), generator=g, device=DEV).bfloat16()
+    want = layer.route(x)
+    for to in (torch.bfloat16, torch.float16):
+        with torch.autocast("cuda", dtype=to):
+            got = layer.route(x)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
