@@ -17,8 +17,9 @@
 // each word of eight weights costs one shift and four logic operations, one
 // for each pair: four bits under the exponent of 1024 are the fp16 number
 // 1024 + q, or 1024 + 16 q where they stand four bits higher.  One half2 add
-// or multiply-add takes off the offset and the zero point.  All of it is
-// exact: q - z is an integer in [-15, 15].  (bf16 has seven bits behind its
+// or multiply-add takes off the offset and the zero point (a published
+// method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run",
+// 2022).  All of it is exact: q - z is an integer in [-15, 15].  (bf16 has seven bits behind its
 // leading one, room for one of the two places: eight integer operations a
 // word instead of five, and 20 % more time where a batch of 32 tokens meets
 // 112 experts' 1024 x 6144.)
@@ -28,8 +29,9 @@
 // Every bf16 down to 2^-30 of the column's largest is then exact in fp16,
 // smaller ones are rounded to a multiple of 2^-38 of it.  The tensor core
 // sums a group's products in fp32, the group's scale multiplies that sum in
-// fp32, and the groups are added in fp32: a warp's, then the warps' in
-// order, CTA by CTA.
+// fp32, and the groups are added in fp32: a warp's, then those of the team's
+// warps in order, then the phases'.  (What passes fp32's end on the way,
+// with scales of 2^95 and more, is computed again behind the items.)
 //
 // Layout.  The weights are read as they are stored.  A warp takes units of
 // 16 R rows x 128 k (64 bytes a row) into its own ring of shared memory with

@@ -400,7 +400,8 @@ int ar_rmsnorm_two_stage_static(const void *const *partials, int n,
  * Route every token to k experts.  For a row x of E logits:
  *   score   s_e = exp(x_e) / sum exp(x)  or  1 / (1 + exp(-x_e))
  *   choice  c_e = s_e + bias_e (without a bias the choices rank as the
- *           logits do)
+ *           logits do, but as the 64-bit scores where AR_GROUP_TOP2 drops
+ *           groups: logits whose scores are equal there are then equal)
  *   groups  the E experts are `groups` runs of E/groups; a group's score is
  *           its largest choice or the sum of its two largest, and only the
  *           experts of the topk_groups best groups can be chosen
