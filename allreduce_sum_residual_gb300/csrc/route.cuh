@@ -23,7 +23,7 @@
 // with the same logit and bias are exact ties, which need no second look.
 //
 // Bound by instructions, some 700 a row of 256 experts: 16384 such rows with
-// groups and bias take 16.2 us (52 us with k passes over every lane's choices
+// groups and bias take 16.5 us (52 us with k passes over every lane's choices
 // in place of the keys), where their bytes would take 2.6 us.
 #pragma once
 
@@ -278,13 +278,13 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
           }
 }
 
-// CTAs an SM, by the registers: with six (80) the 16384 rows above take 16.2
-// us, with eight (64), where more than the second look spills, 17.6 us, with
-// five (96) 16.9 us.
+// CTAs an SM, by the registers: with six (80) the 16384 rows above take 16.5
+// us, with eight (64), where more than the second look spills, 17.5 us, with
+// five (96) 17.0 us.
 constexpr int route_ctas(int v) { return v <= 8 ? 6 : v == 16 ? 4 : 2; }
 
 // How experts are ordered: by their logits (a.by_logit), or by their scores
-// with the bias.  The kind of score as a constant: 18.4 -> 16.2 us.
+// with the bias.  The kind of score as a constant took 2.2 us off.
 enum RouteBy { kByLogit, kBySigmoid, kBySoftmax };
 
 template <typename T, int V, RouteBy BY>

@@ -67,7 +67,7 @@ namespace arn {
 constexpr int kW4MaxWarps = 16;  // four a scheduler, 128 registers a thread
 constexpr int kW4PartK = 128;  // k of a unit's part
 // Parts of a unit.  Two where one row tile and one column tile leave little
-// to do for a unit's fixed work (one row, 7168 x 7168: 10.7 us instead of 11.4);
+// to do for a unit's fixed work (one row, 7168 x 7168: 10.8 us, one part 6 % more);
 // not with two column tiles or groups of 32, whose x or scales need the room.
 __host__ __device__ constexpr int w4_parts(int r, int nt, int group) {
   return r == 1 && nt == 1 && group != 32 ? 2 : 1;
@@ -271,7 +271,7 @@ __device__ __forceinline__ int w4_row(const W4Args &a, int block, int lr) {
 
 // This CTA's share of the items (at most 4096 sets x 65536 blocks): of one
 // column set's, where the sets are known to the host (none then unpacks the x
-// of two: 16 x 4096 x 4096 in 12 us against 15 us), else of all.
+// of two: 16 x 4096 x 4096 in 11.2 us against 15 us), else of all.
 template <bool EXPERTS>
 __device__ __forceinline__ void w4_range(const W4Args &a, int nsets, int *first, int *end) {
   unsigned total = nsets * a.row_blocks, i = blockIdx.x, n = gridDim.x, before = 0;
