@@ -287,33 +287,29 @@ __device__ __forceinline__ void w4_range(const W4Args &a, int nsets, int *first,
   *end = *first + static_cast<int>(each + (i < more ? 1u : 0u));
 }
 
-// One output, by one thread: x as it is, a group's products in fp32, times
-// its scale.
+// One output, by one warp: x as it is, eight products at a time in fp32, times
+// their scale.
 template <int ST, bool ZEROS>
 __device__ float w4_dot(const W4Args &a, const uint4 *x, int64_t row) {
-  const int eights = a.K / a.ng / 8;  // of a group
+  const int shift = __ffs(a.K / a.ng / 8) - 1;  // eights of a group: 4, 8 or 16
   const uint32_t *q = reinterpret_cast<const uint32_t *>(a.q + row * (a.K / 2));
   float sum = 0.f;
-#pragma unroll 1
-  for (int i = 0; i < a.ng; ++i) {
-    const int64_t el = row * a.ng + i;
+#pragma unroll 4
+  for (int k8 = threadIdx.x & 31; k8 < a.K / 8; k8 += 32) {
+    const int64_t el = row * a.ng + (k8 >> shift);
     const float s =
         ST == AR_TYPE_F32
             ? __ldg(reinterpret_cast<const float *>(a.scales) + el)
             : __uint_as_float(uint32_t{__ldg(reinterpret_cast<const uint16_t *>(a.scales) + el)} << 16);
     const float z = ZEROS ? static_cast<float>(__ldg(a.zeros + el) & 15) : 8.f;
-    float d = 0.f;
-#pragma unroll 1
-    for (int k8 = i * eights; k8 < (i + 1) * eights; ++k8) {
-      const uint32_t word = __ldg(q + k8);
-      float v[8];
-      unpack8(__ldg(x + k8), v);
+    const uint32_t word = __ldg(q + k8);
+    float v[8], d = 0.f;
+    unpack8(__ldg(x + k8), v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d = fmaf(static_cast<float>(word >> 4 * j & 15u) - z, v[j], d);
-    }
+    for (int j = 0; j < 8; ++j) d = fmaf(static_cast<float>(word >> 4 * j & 15u) - z, v[j], d);
     sum = fmaf(s, d, sum);
   }
-  return sum;
+  return warp_sum(sum);
 }
 
 // This CTA's outputs that are no finite numbers, again.
@@ -323,44 +319,35 @@ __device__ float w4_dot(const W4Args &a, const uint4 *x, int64_t row) {
 // of their registers: the power of two of each product in front of its scale
 // cost 2 to 8 % of every call, a second look at each item's sums 4 %.
 template <int R, int ST, bool ZEROS, bool EXPERTS>
-__device__ __noinline__ void w4_again(const W4Args &a, const int *sets, const int16_t *ids16,
-                                      int *col_pair) {
-  const int lane = threadIdx.x & 31, threads = blockDim.x;
-  int item0, item1;
-  w4_range<EXPERTS>(a, EXPERTS ? sets[a.E] : 0, &item0, &item1);
+__device__ __noinline__ void w4_again(const W4Args &a, const int *sets, const int16_t *ids16) {
+  const int lane = threadIdx.x & 31;
   const int outs = a.act == AR_ACT_SILU_MUL ? 8 * R : 16 * R;
-  int e = 0;
-  for (int item = item0; item < item1; ++item) {
+  int item0, item1, e = 0;
+  w4_range<EXPERTS>(a, EXPERTS ? sets[a.E] : 0, &item0, &item1);
+  for (int item = item0 + (threadIdx.x >> 5); item < item1; item += blockDim.x >> 5) {
     const int set = item / a.row_blocks, block = item - set * a.row_blocks;
     if constexpr (EXPERTS)
       while (sets[e + 1] <= set) ++e;
-    const int skip = (EXPERTS ? set - sets[e] : set) * a.cols;
-    if (item == item0 || block == 0) {  // the set's pairs, in order
-      __syncthreads();
-      if (threadIdx.x < 32) {
-        int seen = 0;
-        for (int p0 = 0; p0 < a.pairs; p0 += 32) {
-          const bool is = p0 + lane < a.pairs && (!EXPERTS || ids16[p0 + lane] == e);
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
-          const int k = seen + __popc(who & ((1u << lane) - 1u)) - skip;
-          if (is && k >= 0 && k < a.cols) col_pair[k] = p0 + lane;
-          seen += __popc(who);
+    int col = -(EXPERTS ? set - sets[e] : set) * a.cols;  // of the next pair of the expert
+    for (int p0 = 0; p0 < a.pairs && col < a.cols; p0 += 32) {
+      uint32_t who = __ballot_sync(
+          0xFFFFFFFFu, p0 + lane < a.pairs && (!EXPERTS || ids16[p0 + lane] == e));
+      for (; who != 0 && col < a.cols; who &= who - 1, ++col) {
+        if (col < 0) continue;
+        const int pair = p0 + __ffs(who) - 1;
+        const uint4 *x = a.x + static_cast<int64_t>(pair / a.k) * (a.K / 8);
+        __nv_bfloat16 *to = a.out + static_cast<int64_t>(pair) * a.width + block * outs;
+        const bool past = lane < outs && block * outs + lane < a.width &&
+                          !(fabsf(__bfloat162float(to[lane])) < INFINITY);
+        for (uint32_t odd = __ballot_sync(0xFFFFFFFFu, past); odd != 0; odd &= odd - 1) {
+          const int o = __ffs(odd) - 1;
+          const int64_t row = static_cast<int64_t>(e) * a.N + block * outs + o;
+          float v = w4_dot<ST, ZEROS>(a, x, row);
+          if (a.act == AR_ACT_SILU_MUL) v = gated(v, w4_dot<ST, ZEROS>(a, x, row + a.width));
+          // x next to its largest may give inf - inf here alone.
+          if (v == v && lane == 0) to[o] = __float2bfloat16_rn(v);
         }
-        if (lane == 0) col_pair[kW4MaxXCols - 1] = min(a.cols, seen - skip);
       }
-      __syncthreads();
-    }
-    const int n = col_pair[kW4MaxXCols - 1];
-    for (int i = threadIdx.x; i < n * outs; i += threads) {
-      const int col = i / outs, row = block * outs + i % outs, pair = col_pair[col];
-      if (row >= a.width) continue;
-      __nv_bfloat16 *to = a.out + static_cast<int64_t>(pair) * a.width + row;
-      if (fabsf(__bfloat162float(*to)) < INFINITY) continue;
-      const uint4 *x = a.x + static_cast<int64_t>(pair / a.k) * (a.K / 8);
-      const int64_t at = static_cast<int64_t>(e) * a.N + row;
-      float v = w4_dot<ST, ZEROS>(a, x, at);
-      if (a.act == AR_ACT_SILU_MUL) v = gated(v, w4_dot<ST, ZEROS>(a, x, at + a.width));
-      if (v == v) *to = __float2bfloat16_rn(v);  // x next to its largest may give inf - inf here alone
     }
   }
 }
@@ -836,7 +823,8 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
           if (fit >> lane & 1u) set_col[lane + 1] = before;
         }
         for (int c = tid; c < kW4MaxXCols; c += threads) {
-          col_top[c] = 0, col_odd[c] = false;
+          col_top[c] = 0;
+          if (u0 == 0) col_odd[c] = false;  // later phases: the same columns
           if constexpr (!EXPERTS) col_pair[c] = set0 * a.cols + c;  // the sets are full but the last
         }
         __syncthreads();
@@ -1062,7 +1050,7 @@ __global__ void __launch_bounds__(kW4MaxWarps * 32, 1) k_w4_matvec(const __grid_
   cp_async_wait<0>();
   if constexpr (ST != AR_TYPE_F16) {
     __syncthreads();
-    if (again) w4_again<R, ST, ZEROS, EXPERTS>(a, sets, ids16, col_pair);
+    if (again) w4_again<R, ST, ZEROS, EXPERTS>(a, sets, ids16);
   }
 }
 

@@ -129,3 +129,33 @@ def test_overflow_keeps_its_sign_next_to_the_largest_x():
     inf = float("inf")
     assert out[:, [0, 1]].tolist() == [[inf, inf]] * 2
     assert bool((out[:, 2] == -64 * 2.0 ** 66).all()) and not bool(out[:, 3].isnan().any())
+
+
+@pytest.mark.parametrize("m,K,N,act", [(16, 6144, 32768, "silu_mul"), (16, 2048, 32768, "none"),
+                                       (1, 7168, 7168, "none")])
+def test_rows_of_nan_take_no_more_time(m, K, N, act):
+    """A padded batch's garbage: its outputs are not taken for sums that passed
+    fp32's end, in whichever phase it lies."""
+    g = gen(86)
+    x = normal(g, m, K)
+    bad = x.clone()
+    bad[m // 2:, [3, K - 5]] = float("nan")
+    bad[m // 2:, 40] = float("inf")
+    only_first, only_last = x.clone(), x.clone()
+    only_first[0, 3], only_last[0, K - 5] = float("nan"), float("inf")
+    q, s, _ = weights4(g, (N,), K, 128, "bf16", False)
+
+    def time(x):
+        best = float("inf")
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(3):
+                arn.ar_w4_matvec(x, q, s, act=act)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    usual = time(x)
+    for other in (bad, only_first, only_last):
+        assert time(other) < 2 * usual
