@@ -19,10 +19,10 @@
 // 1024 + q, or 1024 + 16 q where they stand four bits higher.  One half2 add
 // or multiply-add takes off the offset and the zero point (a published
 // method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run",
-// 2022).  All of it is exact: q - z is an integer in [-15, 15].  (bf16 has seven bits behind its
-// leading one, room for one of the two places: eight integer operations a
-// word instead of five, and 20 % more time where a batch of 32 tokens meets
-// 112 experts' 1024 x 6144.)
+// 2022).  All of it is exact: q - z is an integer in [-15, 15].  (bf16 has
+// seven bits behind its leading one, room for one of the two places: eight
+// integer operations a word instead of five, and 20 % more time where a batch
+// of 32 tokens meets 112 experts' 1024 x 6144.)
 //
 // fp16 for x.  A column of x is scaled by the power of two that brings its
 // largest finite magnitude to [2^13, 2^14), and its sums are scaled back.
@@ -312,12 +312,12 @@ __device__ float w4_dot(const W4Args &a, const uint4 *x, int64_t row) {
   return warp_sum(sum);
 }
 
-// This CTA's outputs that are no finite numbers, again.
-// A scale of 2^95 or more times a sum of x as fp16 can pass fp32's end where
-// the column's power of two would have brought the result back.  (bf16 and
-// fp32 scales; 2^16 is fp16's largest.)  Behind the items, where it takes none
-// of their registers: the power of two of each product in front of its scale
-// cost 2 to 8 % of every call, a second look at each item's sums 4 %.
+// This CTA's outputs that are no finite numbers, again.  A scale of 2^95 or
+// more times a sum of x as fp16 can pass fp32's end where the column's power
+// of two would have brought the result back.  (bf16 and fp32 scales; 2^16 is
+// fp16's largest.)  Behind the items, where it takes none of their registers
+// (0 to 1.8 % of a call): the power of two of each product in front of its
+// scale cost 0 to 8 % of every call, a second look at each item's sums 4 %.
 template <int R, int ST, bool ZEROS, bool EXPERTS>
 __device__ __noinline__ void w4_again(const W4Args &a, const int *sets, const int16_t *ids16) {
   const int lane = threadIdx.x & 31;
