@@ -25,6 +25,11 @@ Names follow the C ABI:
     ar_combine(y, weights, shared=None, slots=None) -> out
     ar_combine_rmsnorm(y, weights, residual, weight, eps, shared=None, slots=None)
         -> (out, residual_out)
+    ar_block_rmsnorm(partials, residual, weight, eps, post_weight=None, gate=None, ...)
+        -> (out, residual_out)
+    ar_block_rmsnorm_i8(the same) -> (q, scales, residual_out)
+    ar_i8_quantize(x) -> (q, scales)
+    ar_i8_matmul(x, x_scales, w, w_scales, act="none", dtype=torch.bfloat16) -> out
     ar_device_status(device, reset),
     ar_selftest_bounded_wait(device, limit_us), ar_strerror(status), ar_version()
 """
@@ -144,6 +149,17 @@ _SIGS = {
     "ar_combine": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _I64, ctypes.c_int, _I64, _VP, _VP]),
     "ar_combine_rmsnorm": (ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_float, _I64,
                                           ctypes.c_int, _I64, _VP, _VP, _VP]),
+    "ar_block_rmsnorm": (ctypes.c_int, [ctypes.POINTER(_VP), ctypes.c_int, ctypes.c_int, _VP, _VP,
+                                        _I64, _I64, ctypes.c_float, _VP, ctypes.c_int,
+                                        ctypes.c_float, _VP, ctypes.c_float, ctypes.c_float, _I64,
+                                        _I64, _VP, _VP, _VP]),
+    "ar_block_rmsnorm_i8": (ctypes.c_int, [ctypes.POINTER(_VP), ctypes.c_int, ctypes.c_int, _VP,
+                                           _VP, _I64, _I64, ctypes.c_float, _VP, ctypes.c_int,
+                                           ctypes.c_float, _VP, ctypes.c_float, ctypes.c_float,
+                                           _I64, _I64, _VP, _VP, _VP, _VP]),
+    "ar_i8_quantize": (ctypes.c_int, [_VP, ctypes.c_int, _I64, _I64, _I64, _VP, _VP, _VP]),
+    "ar_i8_matmul": (ctypes.c_int, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, ctypes.c_int,
+                                    ctypes.c_int, _VP, _VP]),
     "ar_checks_bounds": (ctypes.c_int, []),
     "ar_selftest_bounds": (ctypes.c_int, [ctypes.c_int]),
     "ar_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -458,10 +474,15 @@ GROUP_SCORES = {"max": AR_GROUP_MAX, "top2": AR_GROUP_TOP2}
 ACTS = {"none": AR_ACT_NONE, "silu_mul": AR_ACT_SILU_MUL}
 
 
-# The calls themselves are in experts.py, which imports torch once (this module
-# does so only where a call needs it); loaded on first use.
+AR_I8_MAX_K = 131056
+AR_I8_MAX_N = 1048576
+AR_I8_MAX_ROWS = 4194304
+
+# The calls themselves are in experts.py and dense.py, which import torch once
+# (this module does so only where a call needs it); loaded on first use.
 _EXPERT_CALLS = ("ar_route_experts", "ar_w4_matvec", "ar_w4_matvec_experts", "ar_combine",
                  "ar_combine_rmsnorm")
+_DENSE_CALLS = ("ar_block_rmsnorm", "ar_block_rmsnorm_i8", "ar_i8_quantize", "ar_i8_matmul")
 
 
 def __getattr__(name):
@@ -469,6 +490,11 @@ def __getattr__(name):
         from . import experts
         for call in _EXPERT_CALLS:
             globals()[call] = getattr(experts, call)
+        return globals()[name]
+    if name in _DENSE_CALLS:
+        from . import dense
+        for call in _DENSE_CALLS:
+            globals()[call] = getattr(dense, call)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

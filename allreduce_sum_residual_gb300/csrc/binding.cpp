@@ -1,5 +1,5 @@
-// The expert-layer calls on torch tensors in one step, for the module
-// experts.py: checks, outputs, stream and the C call, without a Python
+// The calls of the expert layer and of a dense layer in 8 bits on torch tensors
+// in one step, for the modules experts.py and dense.py: checks, outputs, stream and the C call, without a Python
 // statement or a ctypes conversion in between.  A decode step makes some five
 // of these calls a layer, whose kernels take 2 us each where a call through
 // ctypes takes the host 13 to 17 us.
@@ -29,6 +29,10 @@ decltype(&ar_w4_matvec) p_matvec = nullptr;
 decltype(&ar_w4_matvec_experts) p_experts = nullptr;
 decltype(&ar_combine) p_combine = nullptr;
 decltype(&ar_combine_rmsnorm) p_combine_norm = nullptr;
+decltype(&ar_block_rmsnorm) p_block_norm = nullptr;
+decltype(&ar_block_rmsnorm_i8) p_block_norm_i8 = nullptr;
+decltype(&ar_i8_quantize) p_quantize = nullptr;
+decltype(&ar_i8_matmul) p_i8_matmul = nullptr;
 
 struct Unusual {};  // thrown where the long way is to be taken
 
@@ -287,22 +291,145 @@ PyObject *combine_rmsnorm(PyObject *, PyObject *const *v, Py_ssize_t n) {
   });
 }
 
+int type16_code(const at::Tensor &t) {
+  want(t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kHalf);
+  return type_code(t);
+}
+
+// (partials, residual, weight, eps, post_weight, gate, block_scale,
+// residual_scale, weight_offset, bytes, out or q, scales, residual_out) ->
+// (out, residual_out) or (q, scales, residual_out)
+PyObject *block_rmsnorm(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject * {
+    want(PyList_Check(v[0]) || PyTuple_Check(v[0]));
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(v[0]);
+    want(count >= 1 && count <= AR_MAX_RANKS);
+    PyObject **items = PySequence_Fast_ITEMS(v[0]);
+    const at::Tensor &first = tensor(items[0]);
+    const int dev = current_device_of(first);
+    const int type = type16_code(first);
+    const at::ScalarType dtype = first.scalar_type();
+    want(first.dim() == 2);
+    const int64_t m = first.size(0), H = first.size(1);
+    const void *partials[AR_MAX_RANKS];
+    for (Py_ssize_t k = 0; k < count; ++k) partials[k] = input(items[k], dtype, {m, H}, dev);
+    const at::ScalarType rdtype = tensor(v[1]).scalar_type();
+    want(rdtype == dtype || rdtype == at::kFloat);
+    const void *residual = input(v[1], rdtype, {m, H}, dev);
+    const void *weight = input(v[2], dtype, {H}, dev), *post = optional(v[4], dtype, {H}, dev);
+    const float eps = number(v[3]);
+    const void *gate = nullptr;
+    int64_t gate_stride = H, gate_rows = 1;
+    if (v[5] != Py_None) {
+      const at::Tensor &t = tensor(v[5]);
+      want(t.scalar_type() == dtype && t.is_cuda() && t.get_device() == dev);
+      want((t.dim() == 1 || t.dim() == 2) && t.size(-1) == H && (t.stride(-1) == 1 || H <= 1));
+      const int64_t g = t.dim() == 2 ? t.size(0) : 1;
+      want(g >= 1 && m >= 1 && m % g == 0);
+      if (g > 1) gate_stride = t.stride(0);
+      gate_rows = m / g;
+      gate = t.const_data_ptr();
+    }
+    const float block_scale = number(v[6]), residual_scale = number(v[7]), offset = number(v[8]);
+    const bool bytes = v[9] == Py_True;
+    Output out(v[10], bytes ? at::kChar : dtype, {m, H}, first, dev);
+    Output rout(v[12], rdtype, {m, H}, first, dev);
+    const int rtype = rdtype == at::kFloat ? AR_TYPE_F32 : type, parts = static_cast<int>(count);
+    if (!bytes) {
+      call(dev, [&](void *stream) {
+        return p_block_norm(partials, parts, type, post, gate, gate_stride, gate_rows, block_scale,
+                            residual, rtype, residual_scale, weight, offset, eps, m, H, out.p, rout.p,
+                            stream);
+      });
+      return pair(out.t, rout.t);
+    }
+    Output scales(v[11], at::kFloat, {m}, first, dev);
+    call(dev, [&](void *stream) {
+      return p_block_norm_i8(partials, parts, type, post, gate, gate_stride, gate_rows, block_scale,
+                             residual, rtype, residual_scale, weight, offset, eps, m, H,
+                             static_cast<int8_t *>(out.p), static_cast<float *>(scales.p), rout.p,
+                             stream);
+    });
+    PyObject *a = THPVariable_Wrap(out.t), *b = a ? THPVariable_Wrap(scales.t) : nullptr;
+    PyObject *c = b ? THPVariable_Wrap(rout.t) : nullptr;
+    PyObject *all = c ? PyTuple_Pack(3, a, b, c) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    Py_XDECREF(c);
+    return all;
+  });
+}
+
+// (x, q, scales) -> (q, scales)
+PyObject *i8_quantize(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  return guarded(n, 3, [&]() -> PyObject * {
+    const at::Tensor &x = tensor(v[0]);
+    const int dev = current_device_of(x);
+    const int type = type16_code(x);
+    want(x.dim() == 2);
+    const int64_t m = x.size(0), K = x.size(1);
+    want(x.stride(1) == 1 || K <= 1);
+    const int64_t row = m <= 1 ? K : x.stride(0);
+    Output q(v[1], at::kChar, {m, K}, x, dev), scales(v[2], at::kFloat, {m}, x, dev);
+    const void *from = x.const_data_ptr();
+    call(dev, [&](void *stream) {
+      return p_quantize(from, type, row, m, K, static_cast<int8_t *>(q.p),
+                        static_cast<float *>(scales.p), stream);
+    });
+    return pair(q.t, scales.t);
+  });
+}
+
+// (x, x_scales, w, w_scales, act, type, out) -> out
+PyObject *i8_matmul(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject * {
+    const at::Tensor &tx = tensor(v[0]), &tw = tensor(v[2]);
+    const int dev = current_device_of(tx);
+    want(tx.dim() == 2 && tw.dim() == 2);
+    const int64_t m = tx.size(0), K = tx.size(1), N = tw.size(0);
+    const void *x = input(v[0], at::kChar, {m, K}, dev), *xs = input(v[1], at::kFloat, {m}, dev);
+    const void *w = input(v[2], at::kChar, {N, K}, dev), *ws = input(v[3], at::kFloat, {N}, dev);
+    const int act = whole(v[4]), type = whole(v[5]);
+    const at::ScalarType dtype = type == AR_TYPE_F32    ? at::kFloat
+                                 : type == AR_TYPE_BF16 ? at::kBFloat16
+                                                        : at::kHalf;
+    Output out(v[6], dtype, {m, act == AR_ACT_SILU_MUL ? N / 2 : N}, tx, dev);
+    call(dev, [&](void *stream) {
+      return p_i8_matmul(static_cast<const int8_t *>(x), static_cast<const float *>(xs),
+                         static_cast<const int8_t *>(w), static_cast<const float *>(ws), m, N, K, act,
+                         type, out.p, stream);
+    });
+    return THPVariable_Wrap(out.t);
+  });
+}
+
+template <typename F>
+void take(F *&to, void *from) {
+  static_assert(sizeof(to) == sizeof(from), "one address");
+  std::memcpy(&to, &from, sizeof(from));
+}
+
 // Takes the addresses of the library's entry points, in the order above.
 PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t n) {
-  void *at[5];
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "five addresses");
+  constexpr int kCalls = 9;
+  void *at[kCalls];
+  if (n != kCalls) {
+    PyErr_SetString(PyExc_TypeError, "nine addresses");
     return nullptr;
   }
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < kCalls; ++i) {
     at[i] = PyLong_AsVoidPtr(v[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  std::memcpy(&p_route, &at[0], sizeof(void *));
-  std::memcpy(&p_matvec, &at[1], sizeof(void *));
-  std::memcpy(&p_experts, &at[2], sizeof(void *));
-  std::memcpy(&p_combine, &at[3], sizeof(void *));
-  std::memcpy(&p_combine_norm, &at[4], sizeof(void *));
+  take(p_route, at[0]);
+  take(p_matvec, at[1]);
+  take(p_experts, at[2]);
+  take(p_combine, at[3]);
+  take(p_combine_norm, at[4]);
+  take(p_block_norm, at[5]);
+  take(p_block_norm_i8, at[6]);
+  take(p_quantize, at[7]);
+  take(p_i8_matmul, at[8]);
   Py_RETURN_NONE;
 }
 
@@ -318,6 +445,9 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<w4_matvec_experts>("w4_matvec_experts"),
                          method<combine>("combine"),
                          method<combine_rmsnorm>("combine_rmsnorm"),
+                         method<block_rmsnorm>("block_rmsnorm"),
+                         method<i8_quantize>("i8_quantize"),
+                         method<i8_matmul>("i8_matmul"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

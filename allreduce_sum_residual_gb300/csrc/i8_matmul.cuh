@@ -1,0 +1,40 @@
+// Products of 8-bit integers with scales for each token and channel
+// (ar_i8_matmul): the kernels' arguments and what they share.
+//
+//   out[i, j] = xs_i ws_j sum_k x[i, k] w[j, k],  or its gated half
+#pragma once
+
+#include "dense.cuh"
+
+namespace arn {
+
+struct I8Args {
+  const int8_t *x;   // [m, K]
+  const float *xs;   // [m]
+  const int8_t *w;   // [N, K]
+  const float *ws;   // [N]
+  void *out;         // [m, width] of out_type
+  int64_t m, width;  // width: N, or N / 2 with the gated activation
+  int N, K;
+  int gated, out_type;
+  int team;          // matvec: warps of a row block
+  int token_blocks;  // matvec: CTAs beside one another for the tokens
+  int *status;
+};
+
+__device__ __forceinline__ void i8_store(const I8Args &a, int64_t at, float v) {
+  if (a.out_type == AR_TYPE_F32)
+    static_cast<float *>(a.out)[at] = v;
+  else if (a.out_type == AR_TYPE_BF16)
+    static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half *>(a.out)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float silu_mul(float gate, float up) {
+  return gate / (1.f + expf(-gate)) * up;
+}
+
+cudaError_t launch_i8_matvec(I8Args a, int sms, cudaStream_t stream);
+
+}  // namespace arn

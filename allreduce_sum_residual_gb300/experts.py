@@ -30,8 +30,8 @@ _bound_to = None   # the library whose entry points it has
 
 class _LongWay:
     """In the binding's place where there is none for this Python and torch."""
-    route_experts = w4_matvec = w4_matvec_experts = combine = combine_rmsnorm = bind = \
-        staticmethod(lambda *_: None)
+    route_experts = w4_matvec = w4_matvec_experts = combine = combine_rmsnorm = block_rmsnorm = \
+        i8_quantize = i8_matmul = bind = staticmethod(lambda *_: None)
 
 
 def _load_native():
@@ -58,7 +58,8 @@ def _fast():
             _native = _load_native()
         _native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                        (lib.ar_route_experts, lib.ar_w4_matvec, lib.ar_w4_matvec_experts,
-                        lib.ar_combine, lib.ar_combine_rmsnorm)))
+                        lib.ar_combine, lib.ar_combine_rmsnorm, lib.ar_block_rmsnorm,
+                        lib.ar_block_rmsnorm_i8, lib.ar_i8_quantize, lib.ar_i8_matmul)))
         _bound_to = lib
     return _native
 

@@ -526,6 +526,114 @@ int ar_combine_rmsnorm(const void *y, int64_t rows, const int32_t *slots,
                        void *residual_out, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * A dense layer in 8 bits: the epilogue of layers that norm before and after
+ * each block (ar_block_rmsnorm), with its output in 8 bits where an 8-bit
+ * product follows (ar_block_rmsnorm_i8), the same bytes from any other
+ * activations (ar_i8_quantize), and the product (ar_i8_matmul), whose output
+ * is a rank's partial again.
+ *
+ * A row in 8 bits is bytes q in [-127, 127] and one fp32 scale, its largest
+ * magnitude / 127; it stands for q * scale.  A row of zeros has a scale of 0;
+ * a row that holds an infinity or a NaN has a scale of NaN and zeros, so that
+ * whatever is made of it is NaN.
+ *
+ * Streams, graph capture and ownership are those of the expert layer's calls:
+ * asynchronous, no allocation, no state, device memory of the current device.
+ * No output may overlap an input or another output (AR_ERR_ALIAS), but
+ * residual_out may be residual.  m == 0 is a no-op that checks only the sizes
+ * and the options.  Inference only.
+ * --------------------------------------------------------------------------- */
+
+#define AR_I8_MAX_K    131056     /* longest dot product: sums stay below 2^31 */
+#define AR_I8_MAX_N    1048576    /* rows of one 8-bit matrix                  */
+#define AR_I8_MAX_ROWS 4194304    /* tokens of one ar_i8_matmul                */
+
+/*
+ * For each row i < m of H columns:
+ *   s = p_0 + ... + p_{n-1}                                 fp32, rank order
+ *   b = s * rsqrt(mean(s^2) + eps) * (post_weight + weight_offset), or s
+ *       without a post_weight
+ *   b = b * gate[i / gate_rows], or b without a gate
+ *   r = residual_scale * residual + block_scale * b          fp32
+ *   residual_out = r                                        one rounding
+ *   out = r * rsqrt(mean(r^2) + eps) * (weight + weight_offset)
+ * all in fp32 with one rounding to out's type: the norm after a block, its
+ * gate and scale, the residual add and the norm before the next block in one
+ * pass.  With neither post_weight, gate, scales nor offset it is ar_rmsnorm.
+ * The pages have no counterpart of it.
+ *   partials       n arrays [m, H] of `type`, AR_TYPE_BF16 or AR_TYPE_F16;
+ *                  n, H and eps as in ar_rmsnorm.
+ *   post_weight    [H] of `type`, or NULL.    weight  [H] of `type`.
+ *   gate           rows of H of `type`, row g at gate + g * gate_stride
+ *                  elements, or NULL.  Row i takes row i / gate_rows: gate_rows
+ *                  = m is one row for all, the rows of a sequence one for each
+ *                  sequence, 1 one for each token.  gate_stride (a multiple of
+ *                  8, at least H) is not used with a single row.
+ *   residual       [m, H] of residual_type: `type` or AR_TYPE_F32.
+ *   weight_offset  added to both weights in fp32 (1 where a model stores
+ *                  w - 1).
+ *   out            [m, H] of `type`.    residual_out  as residual.
+ * Every array must be 16-byte aligned.  AR_ERR_ARG, AR_ERR_ALIGN,
+ * AR_ERR_UNSUPPORTED or AR_ERR_ALIAS.
+ */
+int ar_block_rmsnorm(const void *const *partials, int n, int type,
+                     const void *post_weight, const void *gate,
+                     int64_t gate_stride, int64_t gate_rows, float block_scale,
+                     const void *residual, int residual_type,
+                     float residual_scale, const void *weight,
+                     float weight_offset, float eps, int64_t m, int64_t H,
+                     void *out, void *residual_out, void *stream);
+
+/*
+ * ar_block_rmsnorm with its output in 8 bits, from the fp32 values (no
+ * rounding to `type` between): q [m, H] bytes and scales [m] (4-byte aligned),
+ * rows in 8 bits as above.  Each q is within 1/2 + 2^-13 of the fp32 value in
+ * units of the scale.  The pages have no counterpart of it.
+ */
+int ar_block_rmsnorm_i8(const void *const *partials, int n, int type,
+                        const void *post_weight, const void *gate,
+                        int64_t gate_stride, int64_t gate_rows,
+                        float block_scale, const void *residual,
+                        int residual_type, float residual_scale,
+                        const void *weight, float weight_offset, float eps,
+                        int64_t m, int64_t H, int8_t *q, float *scales,
+                        void *residual_out, void *stream);
+
+/*
+ * Rows in 8 bits of activations: scale = max|x| / 127 and q = x * 127 / max|x|
+ * rounded to the nearest whole number, halves to even, as exact arithmetic
+ * rounds it (q does not depend on the launch shape).  The pages have no
+ * counterpart of it.
+ *   x       [m, K] of `type`, AR_TYPE_BF16 or AR_TYPE_F16, row i at x + i *
+ *           row_stride elements (row_stride >= K, a multiple of 8).
+ *   K       a multiple of 8, at most AR_MAX_HIDDEN.
+ *   q       [m, K].     scales  [m] fp32, 4-byte aligned.
+ * x and q must be 16-byte aligned.
+ */
+int ar_i8_quantize(const void *x, int type, int64_t row_stride, int64_t m,
+                   int64_t K, int8_t *q, float *scales, void *stream);
+
+/*
+ * out[i, j] = x_scales[i] * w_scales[j] * sum_k x[i, k] w[j, k], or its gated
+ * half (act), rounded once to out's type.  The sum is a whole number; it is
+ * exact while the sums on the way to it stay within 2^24, beyond that each is
+ * rounded to fp32 at worst.  Then two fp32 products, and the activation in
+ * fp32.  The pages have no counterpart of it.
+ *   x         [m, K] bytes in [-128, 127].    x_scales  [m] fp32.
+ *   w         [N, K] bytes in [-128, 127].    w_scales  [N] fp32.
+ *   K         a multiple of 16, at most AR_I8_MAX_K.
+ *   N         1 .. AR_I8_MAX_N; even with AR_ACT_SILU_MUL.
+ *   m         at most AR_I8_MAX_ROWS.
+ *   act       AR_ACT_NONE or AR_ACT_SILU_MUL.
+ *   out       [m, N] of out_type (AR_TYPE_*), or [m, N/2] with
+ *             AR_ACT_SILU_MUL; aligned to its element.
+ * x and w must be 16-byte aligned, the scales 4-byte.
+ */
+int ar_i8_matmul(const int8_t *x, const float *x_scales, const int8_t *w,
+                 const float *w_scales, int64_t m, int64_t N, int64_t K,
+                 int act, int out_type, void *out, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Cross-rank data plane: what the all-reduce needs when the n partials are
  * the buffers of n processes (one per GPU, or several on one GPU).
  *
