@@ -36,5 +36,11 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {
 }
 
 cudaError_t launch_i8_matvec(I8Args a, int sms, cudaStream_t stream);
+// `tokens`: of a tile (16, 32, 64 or 128 of one CTA, 256 of a pair); `split`:
+// CTAs of one CTA's tile.  An AR_* status.
+int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStream_t stream);
+// Shared memory for the tensor kernels, once per device, and the pairs of
+// CTAs that the current device runs at a time.
+int ready_i8_tensor(int sms, int *pairs);
 
 }  // namespace arn

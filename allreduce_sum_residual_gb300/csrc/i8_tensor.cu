@@ -1,0 +1,111 @@
+// The tensor-core products' tensor maps and launches (i8_tensor.cuh).
+#include <mutex>
+
+#include "i8_tensor.cuh"
+
+namespace arn {
+
+static I8Tensor i8_tensor(int type, int tokens, bool gated) {
+  return type == AR_TYPE_F32    ? i8_tensor_f32(tokens, gated)
+         : type == AR_TYPE_BF16 ? i8_tensor_bf16(tokens, gated)
+                                : i8_tensor_f16(tokens, gated);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled g_encode = nullptr;
+
+int ready_i8_tensor(int sms, int *pairs) {
+  static std::mutex mu;
+  static int of_device[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return AR_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (of_device[dev] == 0) {
+    if (g_encode == nullptr) {
+      void *fn = nullptr;
+      cudaDriverEntryPointQueryResult found;
+      if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                           &found) != cudaSuccess ||
+          found != cudaDriverEntryPointSuccess || fn == nullptr) {
+        cudaGetLastError();
+        return AR_ERR_CUDA;
+      }
+      g_encode = reinterpret_cast<EncodeTiled>(fn);
+    }
+    for (int type = AR_TYPE_F32; type <= AR_TYPE_F16; ++type)
+      for (int tokens = 16; tokens <= 256; tokens *= 2)
+        for (int gated = 0; gated < 2; ++gated) {
+          const I8Tensor k = i8_tensor(type, tokens, gated != 0);
+          if (cudaFuncSetAttribute(reinterpret_cast<const void *>(k.kernel),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
+            cudaGetLastError();
+            return AR_ERR_CUDA;
+          }
+        }
+    // Pairs need two SMs of one cluster of the device; some SMs may have no
+    // partner.
+    const I8Tensor k = i8_tensor(AR_TYPE_BF16, 256, false);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(k.threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return AR_ERR_CUDA;
+    }
+    of_device[dev] = n;
+  }
+  *pairs = of_device[dev];
+  return AR_OK;
+}
+
+// Rows of K bytes as boxes of `box` rows x 128 bytes, 128-byte swizzle.
+static bool encode(CUtensorMap *map, const int8_t *p, int64_t K, int64_t rows, int box) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t boxes[2] = {kI8StepK, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(p), dims, strides, boxes,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStream_t stream) {
+  const I8Tensor k = i8_tensor(a.out_type, tokens, a.gated != 0);
+  const bool pair = tokens == 256;
+  I8TensorArgs t;
+  t.a = a;
+  if (!encode(&t.w_map, a.w, a.K, a.N, 64) || !encode(&t.x_map, a.x, a.K, a.m, k.x_rows))
+    return AR_ERR_CUDA;
+  const int64_t channels = (a.gated ? 64 : 128) * (pair ? 2 : 1);
+  const int64_t tiles_n = (a.width + channels - 1) / channels, tiles_m = (a.m + tokens - 1) / tokens;
+  t.tiles_n = static_cast<int>(tiles_n);
+  t.tiles_m = static_cast<int>(tiles_m);
+  t.split = pair ? 1 : split;
+  t.group = 8;
+  t.wait_limit_ns = kWaitLimitNs;
+  const int64_t tiles = tiles_n * tiles_m;
+  int64_t grid = tiles * t.split;
+  if (pair) grid = (tiles < pairs ? tiles : pairs) * 2;
+  if (grid > INT32_MAX) return AR_ERR_UNSUPPORTED;
+  return launch_pdl(k.kernel, t, grid, k.threads, static_cast<size_t>(k.smem), pair ? 2 : t.split,
+                    stream) == cudaSuccess
+             ? AR_OK
+             : AR_ERR_CUDA;
+}
+
+}  // namespace arn

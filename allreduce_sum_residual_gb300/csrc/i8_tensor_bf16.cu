@@ -1,0 +1,7 @@
+#include "i8_tensor.cuh"
+
+namespace arn {
+
+I8Tensor i8_tensor_bf16(int tokens, bool gated) { return i8_tensor_of<__nv_bfloat16>(tokens, gated); }
+
+}  // namespace arn

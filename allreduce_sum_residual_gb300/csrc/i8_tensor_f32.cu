@@ -1,0 +1,7 @@
+#include "i8_tensor.cuh"
+
+namespace arn {
+
+I8Tensor i8_tensor_f32(int tokens, bool gated) { return i8_tensor_of<float>(tokens, gated); }
+
+}  // namespace arn
