@@ -14,21 +14,21 @@
 //
 // The operands are unpacked on the way.  TMA brings boxes of 64 rows x 128
 // bytes of w and TB x 128 of x (128-byte swizzle; what lies behind the arrays'
-// ends comes as zeros, which add nothing).  Four warps turn the tile of w into
+// ends comes as zeros, which add nothing).  Four warps turn a stage of w into
 // fp16 in tensor memory, from where the tensor core takes its A operand: a
 // thread is a row, as in tensor memory, so unpacked weights, twice the bytes,
-// never pass through shared memory.  The others turn x into the swizzled fp16
+// never pass through shared memory.  They also turn x into the swizzled fp16
 // tile of the B operand.  A byte b becomes 1024 + (b + 128) by a byte
 // permutation under the exponent of 1024, and one half2 subtraction leaves b
 // (a published method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants
 // Can't Run", 2022).
 //
-// Roles: a thread issues the loads, a thread the products, four warps unpack
-// w, some unpack x, and of a pair four more write the outputs while the next
-// tile's operands are unpacked.  Between them rings of mbarriers, every wait
+// Roles: a thread issues the loads, a thread the products, teams of four warps
+// unpack a stage each in turn, and of a pair four more warps write the outputs
+// while the next tile's operands are unpacked.  Between them rings of mbarriers, every wait
 // bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA
 // takes one tile, or with few tiles a cluster of `split` CTAs takes one, each
-// a part of K, and adds the parts up through the cluster's shared memory in
+// a part of K, and they add the parts up through the cluster's shared memory in
 // the order of their ranks.
 #pragma once
 
@@ -55,24 +55,30 @@ constexpr int kI8RawW = kI8TileRows * kI8StepK;
 template <int NT, bool PAIR>
 struct I8Shape {
   static constexpr int kTokens = PAIR ? NT / 2 : NT;  // tokens whose x this CTA holds
-  static constexpr int kXWarps = kTokens <= 64 ? 2 : 4;
-  static constexpr int kXWarp0 = kXWarps == 2 ? 2 : 8;
-  static constexpr int kWarps = PAIR ? 16 : kXWarps == 2 ? 8 : 12;
+  // Teams of four warps that unpack, and the stages of the rings.  A team
+  // always meets its own raw slots again: loads land in any order, and a wait
+  // on a slot whose last but one load is still another team's to see would
+  // take that load's phase for the one before it.  (Operand slots are given
+  // back in order.)
+  static constexpr int kTeams = PAIR ? 3 : NT == 64 ? 1 : 2;
+  static constexpr int kOps = PAIR || NT <= 32 ? 3 : 2;
+  static constexpr int kRaw = PAIR ? 3 : NT == 64 ? 3 : 4;
+  static_assert(kRaw % kTeams == 0 && kTeams <= kOps, "a team's slots");
+  static constexpr int kOutWarp0 = 4 + 4 * kTeams;    // of a pair's warps that write
+  static constexpr int kWarps = kOutWarp0 + (PAIR ? 4 : 0);
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kOps = PAIR || NT <= 32 ? 3 : 2;  // stages of unpacked operands
-  static constexpr int kRaw = PAIR ? 3 : NT <= 16 ? 5 : NT <= 32 ? 4 : NT <= 64 ? 3 : 4;
   static constexpr int kRawX = kTokens * kI8StepK;
   static constexpr int kRawBytes = kI8RawW + kRawX;
   static constexpr int kOpBytes = kTokens * kI8StepK * 2;
   static constexpr int kAccCols = NT < 32 ? 32 : NT;
   static constexpr int kOpCols = kI8StepK / 2;
   static constexpr int kCols = kAccCols + kOps * kOpCols <= 256 ? 256 : 512;
-  static constexpr int kExchange = PAIR ? 2 * 2 * 16 * 64 * 4 : 0;
+  static constexpr int kExchange = PAIR ? 2 * 32 * 64 * 4 : 0;  // two mails of i8_write
   // One CTA a tile: the parts of a tile, in the rings' place.
   static constexpr int kRings = kRaw * kRawBytes + kOps * kOpBytes;
   static constexpr int kSmem = 1024 + kRings + kExchange;
   static constexpr int kCtasPerSm = kCols == 256 && kSmem <= 113 * 1024 ? 2 : 1;
-  static_assert(PAIR || NT * kI8TileRows * 4 <= kRings, "the parts of a tile fit the rings");
+  static_assert(PAIR || 2 * NT * kI8TileRows * 4 <= kRings, "the parts of a tile fit the rings");
   static_assert(kSmem <= 230 * 1024 - 512, "shared memory of a CTA");
   static_assert(kAccCols + kOps * kOpCols <= 512, "tensor memory");
   // CTAs that fit an SM's shared memory together never ask for more tensor
@@ -96,20 +102,25 @@ __device__ __forceinline__ bool i8_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // mbar_wait_bounded for barriers that the cluster's CTAs and the tensor core
-// arrive at.
+// arrive at, many times a tile: the clock, whose reading takes about as long
+// as a stage, is looked at once in 64 tries.
 __device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                         uint64_t limit_ns, int *status) {
-  if (i8_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (i8_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1; !i8_try_wait(bar, parity); ++tries) {
     if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      *abort_flag = 1;
-      if (status) atomicExch(status, AR_ERR_TIMEOUT);
-      return false;
+    if (tries % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > limit_ns) {
+        *abort_flag = 1;
+        if (status) atomicExch(status, AR_ERR_TIMEOUT);
+        return false;
+      }
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ uint32_t i8_mapa(uint32_t addr, uint32_t rank) {
@@ -120,9 +131,12 @@ __device__ __forceinline__ uint32_t i8_mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void i8_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// At another CTA's barrier.  It announces operands that this CTA's own tensor
+// core reads, or reads that have ended, and so needs no release at the
+// cluster's scope, which waits 1000 clocks and more for the thread's accesses
+// to memory (it took 40 % of a pair's time).
 __device__ __forceinline__ void i8_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void i8_load_box(uint32_t dst, const CUtensorMap *map, int x, int y,
@@ -192,15 +206,12 @@ __device__ __forceinline__ void i8_commit(uint32_t bar) {
         : "memory");
 }
 
-__device__ __forceinline__ void i8_tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void i8_tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void i8_tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
@@ -240,6 +251,17 @@ __device__ __forceinline__ void i8_sts(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
+// One lane of a warp whose lanes are all here.  Tensor core and copy
+// instructions issued under it take a few clocks each; under a plain test of
+// the lane number they took 90.
+__device__ __forceinline__ bool i8_elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Four bytes as four fp16, in order.
 __device__ __forceinline__ void i8_unpack(uint32_t v, uint32_t &lo, uint32_t &hi) {
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
@@ -254,7 +276,7 @@ __device__ __forceinline__ void i8_unpack(uint32_t v, uint32_t &lo, uint32_t &hi
 // --- the kernel -----------------------------------------------------------------
 
 struct I8Barriers {
-  uint64_t raw_full[8], raw_empty[8], op_full[4], op_empty[4], acc_full, acc_empty;
+  uint64_t raw_full[4], raw_empty[4], op_full[3], op_empty[3], acc_full, acc_empty, parts;
   uint32_t tmem;
   int abort;
 };
@@ -274,6 +296,71 @@ __device__ __forceinline__ __half i8_out<__half>(float v) {
   return __float2half_rn(v);
 }
 
+// Writes COLS tokens of a thread's channel (`row` of the tile) from their sums:
+// tokens tok0 .. of the output, `xs` the scale of token tok0 + lane.  Gated,
+// rows 0..63 are the gates of rows 64..127, which four warps exchange through
+// `mail` (two buffers of COLS * 64 floats, taken in turn) at barrier 1 or 2:
+// gates give the later half of the tokens away and take the other rows' earlier
+// half, so that every thread writes half.
+template <typename OUT, bool GATED, int COLS>
+__device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[COLS], float ws, float xs,
+                                         int64_t tok0, int64_t ch, int row, float *mail, int barrier) {
+  const bool mine = ch < a.width;
+  const int left = static_cast<int>(a.m - tok0 < COLS ? a.m - tok0 : COLS);
+  OUT *to = static_cast<OUT *>(a.out) + tok0 * a.width + ch;
+  if constexpr (!GATED) {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+      const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
+      if (mine && i < left) to[i * a.width] = i8_out<OUT>(y);
+    }
+  } else {
+    constexpr int kHalf = COLS / 2;
+    const bool is_up = row >= 64;
+    float kept[kHalf];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+      const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
+      if (is_up == (i < kHalf))
+        mail[i * 64 + row % 64] = y;
+      else
+        kept[i % kHalf] = y;
+    }
+    if (barrier == 1)
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    else
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const int at = is_up ? kHalf + i : i;
+      const float other = mail[at * 64 + row % 64];
+      const float y = is_up ? silu_mul(other, kept[i]) : silu_mul(kept[i], other);
+      if (mine && at < left) to[at * a.width] = i8_out<OUT>(y);
+    }
+  }
+}
+
+// Whether all of four warps are `fine` (at barrier 1 or 2): a wait that one of them gave up ends
+// all their parts in the barriers behind it.
+__device__ __forceinline__ bool i8_all_fine(bool fine, int barrier) {
+  uint32_t all;
+  if (barrier == 1)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(fine ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(fine ? 1u : 0u)
+        : "memory");
+  return all != 0;
+}
+
 template <typename OUT, int NT, bool PAIR, bool GATED>
 __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>::kCtasPerSm)
     k_i8_tensor(const __grid_constant__ I8TensorArgs t) {
@@ -282,27 +369,29 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   constexpr int kChannels = GATED ? 64 : 128;  // outputs' channels of a CTA's tile
   extern __shared__ char smem_raw[];
   __shared__ I8Barriers bars;
+  __shared__ float xs_of[PAIR ? 1 : NT];
   const I8Args &a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR || t.split > 1 ? cluster_ctarank() : 0;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  float *const ring = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)));
   const uint32_t ops = base + Shape::kRaw * Shape::kRawBytes;
   volatile int *abort = &bars.abort;
   int *status = a.status;
   const uint64_t limit = t.wait_limit_ns;
 
-  constexpr int kUnpackers = 4 + Shape::kXWarps;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Shape::kRaw; ++i) {
       mbar_init(&bars.raw_full[i], 1);
-      mbar_init(&bars.raw_empty[i], kUnpackers);
+      mbar_init(&bars.raw_empty[i], 4);
     }
     for (int i = 0; i < Shape::kOps; ++i) {
-      mbar_init(&bars.op_full[i], kUnpackers * kGroup);
+      mbar_init(&bars.op_full[i], 4 * kGroup);
       mbar_init(&bars.op_empty[i], 1);
     }
     mbar_init(&bars.acc_full, 1);
     mbar_init(&bars.acc_empty, 4 * kGroup);
+    mbar_init(&bars.parts, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&t.w_map) : "memory");
@@ -311,6 +400,33 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   // Before the next grid may start: the CTAs of one grid never wait for tensor
   // memory that the next one's hold.
   if (warp == 1) i8_tmem_alloc<PAIR>(smem_addr(&bars.tmem), Shape::kCols);
+
+  // This CTA's k steps and tiles.
+  const int steps = (a.K + kI8StepK - 1) / kI8StepK;
+  const int step0 = PAIR ? 0 : steps * static_cast<int>(rank) / t.split;
+  const int step1 = PAIR ? steps : steps * static_cast<int>(rank + 1) / t.split;
+  const int tiles = t.tiles_n * t.tiles_m;
+  const int tile0 = static_cast<int>(blockIdx.x) / (PAIR ? 2 : t.split);
+  const int tile_step = PAIR ? static_cast<int>(gridDim.x) / 2 : tiles;
+  const int total = (tiles - tile0 + tile_step - 1) / tile_step * (step1 - step0);  // stages
+  // Tile -> (tile of channels, tile of tokens): pairs walk `group` token tiles
+  // together over all channels, whose x then stays in L2.
+  auto place = [&](int tile, int &tn, int &tm) {
+    if constexpr (PAIR) {
+      const int span = t.group * t.tiles_n;
+      const int g = tile / span, rest = tile - g * span;
+      const int width = min(t.group, t.tiles_m - g * t.group);
+      tn = rest / width;
+      tm = g * t.group + rest - tn * width;
+    } else {
+      tm = tile / t.tiles_n;
+      tn = tile - tm * t.tiles_n;
+    }
+  };
+  const uint32_t raw_full = smem_addr(bars.raw_full), raw_empty = smem_addr(bars.raw_empty);
+  const uint32_t op_full = smem_addr(bars.op_full), op_empty = smem_addr(bars.op_empty);
+  const uint32_t acc_full = smem_addr(&bars.acc_full), acc_empty = smem_addr(&bars.acc_empty);
+
   i8_fence_before();
   if (PAIR || t.split > 1) {
     cluster_arrive_release();
@@ -322,80 +438,50 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
-  // This CTA's k steps and tiles.
-  const int steps = (a.K + kI8StepK - 1) / kI8StepK;
-  int step0 = 0, step1 = steps;
-  if (!PAIR) {
-    step0 = static_cast<int>(static_cast<int64_t>(steps) * rank / t.split);
-    step1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / t.split);
-  }
-  const int64_t tiles = static_cast<int64_t>(t.tiles_n) * t.tiles_m;
-  const int64_t tile0 = PAIR ? blockIdx.x / 2 : blockIdx.x / t.split;
-  const int64_t tile_step = PAIR ? gridDim.x / 2 : tiles;
-  // Tile -> (tile of channels, tile of tokens): pairs walk `group` token tiles
-  // together over all channels, whose x then stays in L2.
-  auto place = [&](int64_t tile, int &tn, int &tm) {
-    if constexpr (PAIR) {
-      const int64_t span = static_cast<int64_t>(t.group) * t.tiles_n;
-      const int g = static_cast<int>(tile / span);
-      const int rest = static_cast<int>(tile - g * span);
-      const int width = min(t.group, t.tiles_m - g * t.group);
-      tm = g * t.group + rest % width;
-      tn = rest / width;
-    } else {
-      tn = static_cast<int>(tile % t.tiles_n);
-      tm = static_cast<int>(tile / t.tiles_n);
-    }
-  };
-
-  const uint32_t raw_full = smem_addr(bars.raw_full), raw_empty = smem_addr(bars.raw_empty);
-  const uint32_t op_full = smem_addr(bars.op_full), op_empty = smem_addr(bars.op_empty);
-  const uint32_t acc_full = smem_addr(&bars.acc_full), acc_empty = smem_addr(&bars.acc_empty);
-
   if (warp == 0) {
     // ---- loads
-    if (lane == 0) {
-      int r = 0, issued = 0;
-      uint32_t phase = 0;
-      bool fine = true;
-      for (int64_t tile = tile0; fine && tile < tiles; tile += tile_step) {
-        int tn, tm;
-        place(tile, tn, tm);
-        const int ch = (PAIR ? tn * 2 + static_cast<int>(rank) : tn) * kChannels;
-        const int tok = tm * NT + (PAIR ? static_cast<int>(rank) * Shape::kTokens : 0);
-        for (int s = step0; s < step1; ++s) {
-          fine = i8_wait(raw_empty + r * 8, phase ^ 1, abort, limit, status);
-          if (!fine) break;
+    int r = 0, issued = 0;
+    uint32_t phase = 0;
+    bool fine = true;
+    for (int tile = tile0; fine && tile < tiles; tile += tile_step) {
+      int tn, tm;
+      place(tile, tn, tm);
+      const int ch = (PAIR ? tn * 2 + static_cast<int>(rank) : tn) * kChannels;
+      const int ch2 = GATED ? static_cast<int>(a.width) + ch : ch + 64;
+      const int tok = tm * NT + (PAIR ? static_cast<int>(rank) * Shape::kTokens : 0);
+      for (int s = step0; s < step1; ++s) {
+        fine = __all_sync(0xFFFFFFFFu, i8_wait(raw_empty + r * 8, phase ^ 1, abort, limit, status));
+        if (!fine) break;
+        if (i8_elect()) {
           const uint32_t to = base + r * Shape::kRawBytes, bar = raw_full + r * 8;
-          mbar_arrive_expect_tx(&bars.raw_full[r], Shape::kRawBytes);
           const int k = s * kI8StepK;
+          mbar_arrive_expect_tx(&bars.raw_full[r], Shape::kRawBytes);
           i8_load_box(to, &t.w_map, k, ch, bar);
-          i8_load_box(to + 64 * kI8StepK, &t.w_map, k, GATED ? static_cast<int>(a.width) + ch : ch + 64,
-                      bar);
+          i8_load_box(to + 64 * kI8StepK, &t.w_map, k, ch2, bar);
           i8_load_box(to + kI8RawW, &t.x_map, k, tok, bar);
-          if (issued < Shape::kRaw) ++issued;
-          if (++r == Shape::kRaw) {
-            r = 0;
-            phase ^= 1;
-          }
+        }
+        if (issued < Shape::kRaw) ++issued;
+        if (++r == Shape::kRaw) {
+          r = 0;
+          phase ^= 1;
         }
       }
-      if (!fine) {
-        // Loads in flight land before this CTA's memory goes.
-        int never = 0;
-        for (int i = 0; i < issued; ++i) {
-          if (--r < 0) {
-            r = Shape::kRaw - 1;
-            phase ^= 1;
-          }
-          i8_wait(raw_full + r * 8, phase, &never, limit, status);
+    }
+    if (!fine) {
+      // Loads in flight land before this CTA's memory goes.
+      int never = 0;
+      for (int i = 0; i < issued; ++i) {
+        if (--r < 0) {
+          r = Shape::kRaw - 1;
+          phase ^= 1;
         }
+        i8_wait(raw_full + r * 8, phase, &never, limit, status);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---- products
-    if (lane == 0 && rank % kGroup == 0) {
+    if (!PAIR || rank == 0) {
       // Instruction descriptor: fp32 sums, fp16 operands, both along k.
       constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) |
                                  (static_cast<uint32_t>(PAIR ? 16 : 8) << 24);
@@ -406,310 +492,250 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       int s = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool fine = true;
-      for (int64_t tile = tile0; fine && tile < tiles; tile += tile_step) {
+      for (int tile = tile0; fine && tile < tiles; tile += tile_step) {
         if (PAIR) {
-          fine = i8_wait(acc_empty, acc_phase ^ 1, abort, limit, status);
+          fine = __all_sync(0xFFFFFFFFu, i8_wait(acc_empty, acc_phase ^ 1, abort, limit, status));
           if (!fine) break;
-          i8_fence_after();
         }
         for (int step = step0; step < step1; ++step) {
-          fine = i8_wait(op_full + s * 8, phase, abort, limit, status);
+          fine = __all_sync(0xFFFFFFFFu, i8_wait(op_full + s * 8, phase, abort, limit, status));
           if (!fine) break;
           i8_fence_after();
-          const uint32_t b = ops + s * Shape::kOpBytes;
-          const uint32_t at = tmem + Shape::kAccCols + s * Shape::kOpCols;
+          if (i8_elect()) {
+            const uint32_t b = ops + s * Shape::kOpBytes;
+            const uint32_t at = tmem + Shape::kAccCols + s * Shape::kOpCols;
 #pragma unroll
-          for (int ks = 0; ks < kI8StepK / 16; ++ks) {
-            const uint32_t from = b + (ks >> 2) * (Shape::kTokens * 128) + (ks & 3) * 32;
-            i8_mma<PAIR>(tmem, at + ks * 8, kDesc | ((from >> 4) & 0x3FFF), idesc,
-                         step > step0 || ks > 0);
+            for (int ks = 0; ks < kI8StepK / 16; ++ks) {
+              const uint32_t from = b + (ks >> 2) * (Shape::kTokens * 128) + (ks & 3) * 32;
+              i8_mma<PAIR>(tmem, at + ks * 8, kDesc | ((from >> 4) & 0x3FFF), idesc,
+                           step > step0 || ks > 0);
+            }
+            i8_commit<PAIR>(op_empty + s * 8);
+            if (step + 1 == step1) i8_commit<PAIR>(acc_full);
           }
-          i8_commit<PAIR>(op_empty + s * 8);
+          __syncwarp();
           if (++s == Shape::kOps) {
             s = 0;
             phase ^= 1;
           }
         }
-        if (fine) {
-          i8_commit<PAIR>(acc_full);
-          acc_phase ^= 1;
-        }
+        if (fine) acc_phase ^= 1;
       }
       if (!fine) {
         // Products in flight end before their operands go.
         int never = 0;
-        i8_commit<PAIR>(acc_full);
+        if (i8_elect()) i8_commit<PAIR>(acc_full);
+        __syncwarp();
         i8_wait(acc_full, acc_phase, &never, limit, status);
       }
     }
-    __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
-    // ---- w: a thread a row
-    const int row = (warp - 4) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(warp - 4) << 21;  // 32 lanes a warp
-    const uint32_t leader = PAIR ? i8_mapa(op_full, 0) : 0;
-    int r = 0, s = 0;
-    uint32_t raw_phase = 0, op_phase = 0;
-    bool fine = true;
-    for (int64_t tile = tile0; fine && tile < tiles; tile += tile_step) {
-      for (int step = step0; step < step1; ++step) {
-        fine = i8_wait(raw_full + r * 8, raw_phase, abort, limit, status);
-        if (!__all_sync(0xFFFFFFFFu, fine)) {
-          fine = false;
-          break;
-        }
-        uint4 v[8];
-        const uint32_t from = base + r * Shape::kRawBytes + row * kI8StepK;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = i8_lds(from + ((c ^ (row & 7)) << 4));
-        __syncwarp();
-        if (lane == 0) i8_arrive(raw_empty + r * 8);
-        fine = i8_wait(op_empty + s * 8, op_phase ^ 1, abort, limit, status);
-        if (!__all_sync(0xFFFFFFFFu, fine)) {
-          fine = false;
-          break;
-        }
-        i8_fence_after();
-        const uint32_t at = tmem + lanes + Shape::kAccCols + s * Shape::kOpCols;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            i8_unpack(v[h * 4 + c].x, o[c * 8], o[c * 8 + 1]);
-            i8_unpack(v[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
-            i8_unpack(v[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
-            i8_unpack(v[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
-          }
-          i8_tmem_store32(at + h * 32, o);
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        i8_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            i8_arrive_cluster(leader + s * 8);
-          else
-            i8_arrive(op_full + s * 8);
-        }
-        if (++r == Shape::kRaw) {
-          r = 0;
-          raw_phase ^= 1;
-        }
-        if (++s == Shape::kOps) {
-          s = 0;
-          op_phase ^= 1;
-        }
+    if (PAIR) {
+      // The last stages' slots come back too before this CTA's memory goes.
+      for (int i = 0; i < Shape::kOps && i < total; ++i) {
+        const uint32_t n = static_cast<uint32_t>(total - 1 - i);
+        if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
       }
     }
-  } else if (warp >= Shape::kXWarp0 && warp < Shape::kXWarp0 + Shape::kXWarps) {
-    // ---- x: the lanes of a group of eight take eight rows' same bytes
-    constexpr int kThreadsX = Shape::kXWarps * 32;
-    constexpr int kSets = kThreadsX / Shape::kTokens;  // threads of a row
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---- scales of x for the parts' sums
+    if (!PAIR) {
+      int tn, tm;
+      place(tile0, tn, tm);
+      for (int i = threadIdx.x - 64; i < NT; i += 64) {
+        const int64_t tok = static_cast<int64_t>(tm) * NT + i;
+        xs_of[PAIR ? 0 : i] = tok < a.m ? __ldg(a.xs + tok) : 0.f;
+      }
+    }
+  } else if (warp < Shape::kOutWarp0) {
+    // ---- operands: a team takes every kTeams-th stage; a thread unpacks a row
+    // of w, and a row of x or a part of one (the lanes of a group of eight take
+    // the same bytes of eight rows).
+    const int team = (warp - 4) / 4, at = (warp & 3) * 32 + lane;
+    const uint32_t a_lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + Shape::kAccCols;
+    constexpr int kSets = 128 / Shape::kTokens;  // threads of a row of x
     constexpr int kChunks = 8 / kSets;
-    static_assert(kSets >= 1 && kSets <= 8, "threads of a row");
-    const int at = (warp - Shape::kXWarp0) * 32 + lane;
+    static_assert(kSets >= 1 && kSets <= 8, "threads of a row of x");
     const int row = at % Shape::kTokens, set = at / Shape::kTokens;
-    const uint32_t leader = PAIR ? i8_mapa(op_full, 0) : 0;
-    int r = 0, s = 0;
+    const uint32_t w_swizzle = at & 7, x_swizzle = row & 7;
+    const uint32_t leader = PAIR ? i8_mapa(op_full, 0) : 0;  // the CTA that issues the products
+    int r = team, s = team;
     uint32_t raw_phase = 0, op_phase = 0;
-    bool fine = true;
-    for (int64_t tile = tile0; fine && tile < tiles; tile += tile_step) {
-      for (int step = step0; step < step1; ++step) {
-        fine = i8_wait(raw_full + r * 8, raw_phase, abort, limit, status);
-        if (!__all_sync(0xFFFFFFFFu, fine)) {
-          fine = false;
-          break;
-        }
-        uint4 v[kChunks];
-        const uint32_t from = base + r * Shape::kRawBytes + kI8RawW + row * kI8StepK;
+    for (int n = team; n < total; n += Shape::kTeams) {
+      if (!__all_sync(0xFFFFFFFFu, i8_wait(raw_full + r * 8, raw_phase, abort, limit, status))) break;
+      uint4 v[8], x[kChunks];
+      const uint32_t raw = base + r * Shape::kRawBytes;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          v[c] = i8_lds(from + (((set * kChunks + c) ^ (row & 7)) << 4));
-        __syncwarp();
-        if (lane == 0) i8_arrive(raw_empty + r * 8);
-        fine = i8_wait(op_empty + s * 8, op_phase ^ 1, abort, limit, status);
-        if (!__all_sync(0xFFFFFFFFu, fine)) {
-          fine = false;
-          break;
-        }
-        const uint32_t to = ops + s * Shape::kOpBytes + row * 128;
+      for (uint32_t c = 0; c < 8; ++c) v[c] = i8_lds(raw + at * kI8StepK + ((c ^ w_swizzle) << 4));
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int chunk = set * kChunks + c;
-          const uint32_t half = to + (chunk >> 2) * (Shape::kTokens * 128);
-          const uint32_t first = 2 * (chunk & 3);
-          uint32_t o[8];
-          i8_unpack(v[c].x, o[0], o[1]);
-          i8_unpack(v[c].y, o[2], o[3]);
-          i8_unpack(v[c].z, o[4], o[5]);
-          i8_unpack(v[c].w, o[6], o[7]);
-          i8_sts(half + ((first ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-          i8_sts(half + (((first + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+      for (uint32_t c = 0; c < kChunks; ++c)
+        x[c] = i8_lds(raw + kI8RawW + row * kI8StepK + (((set * kChunks + c) ^ x_swizzle) << 4));
+      __syncwarp();
+      if (lane == 0) i8_arrive(raw_empty + r * 8);
+      if (!__all_sync(0xFFFFFFFFu, i8_wait(op_empty + s * 8, op_phase ^ 1, abort, limit, status))) break;
+      i8_fence_after();
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t o[16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          i8_unpack(v[h * 2 + c].x, o[c * 8], o[c * 8 + 1]);
+          i8_unpack(v[h * 2 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
+          i8_unpack(v[h * 2 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
+          i8_unpack(v[h * 2 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
+        }
+        i8_tmem_store16(a_lanes + s * Shape::kOpCols + h * 16, o);
+      }
+      const uint32_t to = ops + s * Shape::kOpBytes + row * 128;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const uint32_t chunk = set * kChunks + c, first = 2 * (chunk & 3);
+        const uint32_t half = to + (chunk >> 2) * (Shape::kTokens * 128);
+        uint32_t o[8];
+        i8_unpack(x[c].x, o[0], o[1]);
+        i8_unpack(x[c].y, o[2], o[3]);
+        i8_unpack(x[c].z, o[4], o[5]);
+        i8_unpack(x[c].w, o[6], o[7]);
+        i8_sts(half + ((first ^ x_swizzle) << 4), o[0], o[1], o[2], o[3]);
+        i8_sts(half + (((first + 1) ^ x_swizzle) << 4), o[4], o[5], o[6], o[7]);
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      i8_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          i8_arrive_cluster(leader + s * 8);
+        else
+          i8_arrive(op_full + s * 8);
+      }
+      r += Shape::kTeams;
+      if (r >= Shape::kRaw) {
+        r -= Shape::kRaw;
+        raw_phase ^= 1;
+      }
+      s += Shape::kTeams;
+      if (s >= Shape::kOps) {
+        s -= Shape::kOps;
+        op_phase ^= 1;
+      }
+    }
+    __syncwarp();
+    if constexpr (!PAIR) {
+      // ---- the sums: a thread a channel, 16 tokens a team in turn.  Every
+      // stage has been read once they are done, and the rings are free.
+      int tn, tm;
+      place(tile0, tn, tm);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+      const int64_t ch = static_cast<int64_t>(tn) * kChannels + (GATED ? at % 64 : at);
+      const int64_t tok = static_cast<int64_t>(tm) * NT;
+      float ws = 0.f, xs[NT / 16];
+      if (t.split == 1) {
+        ws = ch < a.width ? __ldg(a.ws + ch + (GATED && at >= 64 ? a.width : 0)) : 0.f;
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c)
+          xs[c] = lane < 16 && tok + c * 16 + lane < a.m ? __ldg(a.xs + tok + c * 16 + lane) : 0.f;
+      }
+      if (i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), 1 + team)) {
+        i8_fence_after();
+#pragma unroll
+        for (int c = 0; c < NT / 16; ++c) {
+          if (c % Shape::kTeams != team) continue;
+          uint32_t v[16];
+          i8_tmem_load16(acc + c * 16, v);
+          if (t.split == 1) {
+            float *mail = ring + (team * 2 + c / Shape::kTeams % 2) * (16 * 64);
+            i8_write<OUT, GATED, 16>(a, v, ws, xs[c], tok + c * 16, ch, at, mail, 1 + team);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              ring[(c * 16 + i) * kI8TileRows + at] = __uint_as_float(v[i]);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            i8_arrive_cluster(leader + s * 8);
-          else
-            i8_arrive(op_full + s * 8);
-        }
-        if (++r == Shape::kRaw) {
-          r = 0;
-          raw_phase ^= 1;
-        }
-        if (++s == Shape::kOps) {
-          s = 0;
-          op_phase ^= 1;
-        }
       }
     }
-  } else if (PAIR && warp >= 12) {
-    // ---- outputs of a pair's tile: a thread a channel
-    const int q = warp - 12, row = q * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(q) << 21;
+  } else if constexpr (PAIR) {
+    // ---- outputs of a pair's tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t leader_empty = i8_mapa(acc_empty, 0);
-    float *exchange = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)) + Shape::kRings);
-    OUT *out = static_cast<OUT *>(a.out);
+    float *mail = ring + Shape::kRings / 4;
     uint32_t acc_phase = 0;
-    for (int64_t tile = tile0; tile < tiles; tile += tile_step) {
+    for (int tile = tile0; tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
       const int64_t ch = static_cast<int64_t>(tn * 2 + static_cast<int>(rank)) * kChannels +
                          (GATED ? row % 64 : row);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
-      const bool mine = ch < a.width;
-      const float ws = mine ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
-      bool fine = i8_wait(acc_full, acc_phase, abort, limit, status);
-      if (GATED) {  // the four warps meet below: all go on or none
-        uint32_t all;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(all)
-            : "r"(fine ? 1u : 0u)
-            : "memory");
-        fine = all != 0;
-      }
-      if (!__all_sync(0xFFFFFFFFu, fine)) break;
+      const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
+      float xs[NT / 32];
+#pragma unroll
+      for (int c = 0; c < NT / 32; ++c)
+        xs[c] = tok + c * 32 + lane < a.m ? __ldg(a.xs + tok + c * 32 + lane) : 0.f;
+      if (!i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 1)) break;
       acc_phase ^= 1;
       i8_fence_after();
-#pragma unroll 1
-      for (int cb = 0; cb < NT / 32; ++cb) {
+#pragma unroll
+      for (int c = 0; c < NT / 32; ++c) {
         uint32_t v[32];
-        i8_tmem_load32(tmem + lanes + cb * 32, v);
-        if (cb == NT / 32 - 1) {
+        i8_tmem_load32(acc + c * 32, v);
+        if (c == NT / 32 - 1) {
           i8_fence_before();
           __syncwarp();
           if (lane == 0) i8_arrive_cluster(leader_empty);
         }
-        const int64_t tok0 = tok + cb * 32;
-        const int left = static_cast<int>(a.m - tok0 < 32 ? a.m - tok0 : 32);
-        const float xs = lane < left ? __ldg(a.xs + tok0 + lane) : 0.f;
-        OUT *to = out + tok0 * a.width + ch;
-        if constexpr (!GATED) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
-            if (mine && i < left) to[i * a.width] = i8_out<OUT>(y);
-          }
-        } else {
-          // Gate rows give the later 16 tokens away and take the up rows'
-          // earlier 16, so that every thread writes half.
-          const bool is_up = row >= 64;
-          float *mail = exchange + (cb & 1) * (2 * 16 * 64);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
-            v[i] = __float_as_uint(y);
-            if (is_up == (i < 16)) mail[((is_up ? 0 : 16) + i % 16) * 64 + row % 64] = y;
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = is_up ? 16 + i : i;
-            const float other = mail[at * 64 + row % 64];
-            const float mine_v = __uint_as_float(is_up ? v[16 + i] : v[i]);
-            const float y = is_up ? silu_mul(other, mine_v) : silu_mul(mine_v, other);
-            if (mine && at < left) to[at * a.width] = i8_out<OUT>(y);
-          }
-        }
+        i8_write<OUT, GATED, 32>(a, v, ws, xs[c], tok + c * 32, ch, row, mail + (c & 1) * (32 * 64), 1);
       }
     }
   }
   __syncwarp();
 
   if constexpr (!PAIR) {
-    // ---- outputs of one CTA's tile, or of its part of the tokens: the parts
-    // [rank][token][128 channels] of a tile's split, in rank order.
-    int tn, tm;
-    place(tile0, tn, tm);
-    const int S = t.split, cols = NT / S;
-    bool fine = true;
-    if (warp >= 4 && warp < 8) {
-      fine = i8_wait(acc_full, 0, abort, limit, status);
-      fine = __all_sync(0xFFFFFFFFu, fine);
-      i8_fence_after();
-    }
-    // Every CTA's rings are idle.
-    if (S > 1) {
-      cluster_arrive_release();
+    if (t.split > 1) {
+      // ---- the parts of a tile: each CTA has its own [token][128 channels] in
+      // its ring, and sends each CTA of the cluster that one's share of the
+      // tokens, which sums them in the order of the ranks.
+      const int S = t.split, cols = NT / S;
+      const uint32_t share = static_cast<uint32_t>(cols) * kI8TileRows * 4;
+      const uint32_t inbox = base + NT * kI8TileRows * 4, parts = smem_addr(&bars.parts);
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars.parts, S * share);
+      int tn, tm;
+      place(tile0, tn, tm);
+      const int l = threadIdx.x % kChannels;
+      const int64_t ch = static_cast<int64_t>(tn) * kChannels + l;
+      const int64_t tok0 = static_cast<int64_t>(tm) * NT + rank * cols;
+      const float ws = ch < a.width ? __ldg(a.ws + ch) : 0.f;
+      const float ws_up = GATED && ch < a.width ? __ldg(a.ws + ch + a.width) : 0.f;
+      cluster_arrive_release();  // the rings of all are free, the parts written
       cluster_wait_acquire();
-    } else {
-      __syncthreads();
-    }
-    if (warp >= 4 && warp < 8 && fine) {
-      const uint32_t lanes = static_cast<uint32_t>(warp - 4) << 21;
-      const uint32_t row = base + ((warp - 4) * 32 + lane) * 4;
-#pragma unroll 1
-      for (int c0 = 0; c0 < NT; c0 += 16) {
-        uint32_t v[16];
-        i8_tmem_load16(tmem + lanes + c0, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int owner = (c0 + i) / cols, col = (c0 + i) % cols;
-          const uint32_t at = row + (rank * cols + col) * (kI8TileRows * 4);
-          if (S > 1)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(i8_mapa(at, owner)), "r"(v[i])
-                         : "memory");
-          else
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v[i]) : "memory");
+      if (threadIdx.x < S && !*abort)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+            ::"r"(i8_mapa(inbox + rank * share, threadIdx.x)), "r"(base + threadIdx.x * share), "r"(share),
+            "r"(i8_mapa(parts, threadIdx.x))
+            : "memory");
+      if (i8_wait(parts, 0, abort, limit, status)) {
+        const float *from = ring + NT * kI8TileRows + l;
+        OUT *out = static_cast<OUT *>(a.out);
+        for (int col = threadIdx.x / kChannels; col < cols; col += Shape::kThreads / kChannels) {
+          float y = 0.f, up = 0.f;
+          for (int p = 0; p < S; ++p) {
+            y += from[(p * cols + col) * kI8TileRows];
+            if (GATED) up += from[(p * cols + col) * kI8TileRows + 64];
+          }
+          const float xs = xs_of[rank * cols + col];
+          y = y * ws * xs;
+          if (GATED) y = silu_mul(y, up * ws_up * xs);
+          if (ch < a.width && tok0 + col < a.m) out[(tok0 + col) * a.width + ch] = i8_out<OUT>(y);
         }
       }
-    }
-    if (S > 1) {
-      cluster_arrive_release();
-      cluster_wait_acquire();
-    } else {
-      __syncthreads();
-    }
-    const float *parts =
-        reinterpret_cast<const float *>(smem_raw + (base - smem_addr(smem_raw)));
-    OUT *out = static_cast<OUT *>(a.out);
-    const int64_t ch0 = static_cast<int64_t>(tn) * kChannels;
-    const int64_t tok0 = static_cast<int64_t>(tm) * NT + rank * cols;
-    if (!bars.abort) {
-      for (int i = threadIdx.x; i < cols * kChannels; i += Shape::kThreads) {
-        const int l = i % kChannels, col = i / kChannels;
-        const int64_t ch = ch0 + l, tok = tok0 + col;
-        if (ch >= a.width || tok >= a.m) continue;
-        float y = 0.f, up = 0.f;
-        for (int p = 0; p < S; ++p) {
-          const float *from = parts + (p * cols + col) * kI8TileRows + l;
-          y += from[0];
-          if (GATED) up += from[64];
-        }
-        const float xs = __ldg(a.xs + tok);
-        y = y * __ldg(a.ws + ch) * xs;
-        if (GATED) y = silu_mul(y, up * __ldg(a.ws + ch + a.width) * xs);
-        out[tok * a.width + ch] = i8_out<OUT>(y);
-      }
+      __syncwarp();
     }
   }
-  // Nobody leaves while its pair may still use its memory.
+  // Nobody leaves while its cluster may still use its memory.
   i8_fence_before();
-  if (PAIR) {
+  if (PAIR || t.split > 1) {
     cluster_arrive_release();
     cluster_wait_acquire();
   }
