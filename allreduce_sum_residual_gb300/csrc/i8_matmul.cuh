@@ -17,6 +17,7 @@ struct I8Args {
   int64_t m, width;  // width: N, or N / 2 with the gated activation
   int N, K;
   int gated, out_type;
+  int aligned;       // tensor cores: rows of out start and end at 16 bytes
   int team;          // matvec: warps of a row block
   int token_blocks;  // matvec: CTAs beside one another for the tokens
   int *status;
@@ -31,8 +32,12 @@ __device__ __forceinline__ void i8_store(const I8Args &a, int64_t at, float v) {
     static_cast<__half *>(a.out)[at] = __float2half_rn(v);
 }
 
+// gate / (1 + exp(-gate)) * up; the reciprocal is within a step (of any
+// divisor up to infinity, where it is 0).
 __device__ __forceinline__ float silu_mul(float gate, float up) {
-  return gate / (1.f + expf(-gate)) * up;
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + expf(-gate)));
+  return gate * r * up;
 }
 
 cudaError_t launch_i8_matvec(I8Args a, int sms, cudaStream_t stream);

@@ -89,6 +89,7 @@ int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStre
   const bool pair = tokens == 256;
   I8TensorArgs t;
   t.a = a;
+  t.a.aligned = aligned16(a.out) && a.width * type_size(a.out_type) % 16 == 0;
   if (!encode(&t.w_map, a.w, a.K, a.N, 64) || !encode(&t.x_map, a.x, a.K, a.m, k.x_rows))
     return AR_ERR_CUDA;
   const int64_t channels = (a.gated ? 64 : 128) * (pair ? 2 : 1);

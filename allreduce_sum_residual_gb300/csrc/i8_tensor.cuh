@@ -73,13 +73,14 @@ struct I8Shape {
   static constexpr int kAccCols = NT < 32 ? 32 : NT;
   static constexpr int kOpCols = kI8StepK / 2;
   static constexpr int kCols = kAccCols + kOps * kOpCols <= 256 ? 256 : 512;
-  static constexpr int kExchange = PAIR ? 2 * 32 * 64 * 4 : 0;  // two mails of i8_write
+  static constexpr int kBuffer = (PAIR ? 32 : 16) * 128 * 4;    // one of i8_write's
+  static constexpr int kExchange = PAIR ? 2 * kBuffer : 0;
   // One CTA a tile: the parts of a tile, in the rings' place.
   static constexpr int kRings = kRaw * kRawBytes + kOps * kOpBytes;
   static constexpr int kSmem = 1024 + kRings + kExchange;
   static constexpr int kCtasPerSm = kCols == 256 && kSmem <= 113 * 1024 ? 2 : 1;
   static_assert(PAIR || 2 * NT * kI8TileRows * 4 <= kRings, "the parts of a tile fit the rings");
-  static_assert(kSmem <= 230 * 1024 - 512, "shared memory of a CTA");
+  static_assert(kSmem + NT * 4 + (PAIR ? 0 : 512) + 256 <= 227 * 1024, "shared memory of a CTA");
   static_assert(kAccCols + kOps * kOpCols <= 512, "tensor memory");
   // CTAs that fit an SM's shared memory together never ask for more tensor
   // memory than it has, whichever of these kernels they are of: an allocation
@@ -262,6 +263,16 @@ __device__ __forceinline__ bool i8_elect() {
   return one != 0;
 }
 
+// The cluster's barrier where nothing but the reads and copies that its threads
+// have waited for is ordered by it: with a release an arrival waits for the
+// thread's stores to memory, 2000 clocks.
+__device__ __forceinline__ void i8_cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void i8_cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Four bytes as four fp16, in order.
 __device__ __forceinline__ void i8_unpack(uint32_t v, uint32_t &lo, uint32_t &hi) {
   const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
@@ -296,46 +307,83 @@ __device__ __forceinline__ __half i8_out<__half>(float v) {
   return __float2half_rn(v);
 }
 
-// Writes COLS tokens of a thread's channel (`row` of the tile) from their sums:
-// tokens tok0 .. of the output, `xs` the scale of token tok0 + lane.  Gated,
-// rows 0..63 are the gates of rows 64..127, which four warps exchange through
-// `mail` (two buffers of COLS * 64 floats, taken in turn) at barrier 1 or 2:
-// gates give the later half of the tokens away and take the other rows' earlier
-// half, so that every thread writes half.
+__device__ __forceinline__ void i8_team_sync(int barrier) {
+  if (barrier == 1)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+
+// Eight, or four fp32, outputs in a row.
+template <typename OUT>
+__device__ __forceinline__ uint4 i8_pack(const float *y);
+template <>
+__device__ __forceinline__ uint4 i8_pack<float>(const float *y) {
+  return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                    __float_as_uint(y[3]));
+}
+template <>
+__device__ __forceinline__ uint4 i8_pack<__nv_bfloat16>(const float *y) {
+  const float f[8] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+  return pack16<__nv_bfloat16>(f);
+}
+template <>
+__device__ __forceinline__ uint4 i8_pack<__half>(const float *y) {
+  const float f[8] = {y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]};
+  return pack16<__half>(f);
+}
+
+// Writes COLS tokens of a tile's channels from the sums: four warps, a thread
+// a channel (`row` of the tile, scale `ws`), tokens tok0 .. of the output with
+// the scales xs[0 ..].  The outputs pass through shared memory, `buf` (two
+// buffers, taken in turn), so that a token's channels leave in 16-byte pieces
+// (as 2 bytes a lane they took three times as long).  Gated, rows 0..63 are the
+// gates of rows 64..127: they give the later half of the tokens away and take
+// the other rows' earlier half, and every thread computes half.
 template <typename OUT, bool GATED, int COLS>
-__device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[COLS], float ws, float xs,
-                                         int64_t tok0, int64_t ch, int row, float *mail, int barrier) {
-  const bool mine = ch < a.width;
-  const int left = static_cast<int>(a.m - tok0 < COLS ? a.m - tok0 : COLS);
-  OUT *to = static_cast<OUT *>(a.out) + tok0 * a.width + ch;
+__device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[COLS], float ws,
+                                         const float *xs, int64_t tok0, int64_t ch0, int row, char *buf,
+                                         int barrier) {
+  constexpr int kCh = GATED ? 64 : 128, kPiece = 16 / sizeof(OUT);
+  float *mail = reinterpret_cast<float *>(buf);
+  OUT *stage = reinterpret_cast<OUT *>(buf + (GATED ? COLS * 64 * 4 : 0));
   if constexpr (!GATED) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-      const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
-      if (mine && i < left) to[i * a.width] = i8_out<OUT>(y);
-    }
+    for (int i = 0; i < COLS; ++i) stage[i * kCh + row] = i8_out<OUT>(__uint_as_float(v[i]) * ws * xs[i]);
   } else {
     constexpr int kHalf = COLS / 2;
     const bool is_up = row >= 64;
     float kept[kHalf];
 #pragma unroll
     for (int i = 0; i < COLS; ++i) {
-      const float y = __uint_as_float(v[i]) * ws * __shfl_sync(0xFFFFFFFFu, xs, i);
+      const float y = __uint_as_float(v[i]) * ws * xs[i];
       if (is_up == (i < kHalf))
         mail[i * 64 + row % 64] = y;
       else
         kept[i % kHalf] = y;
     }
-    if (barrier == 1)
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    else
-      asm volatile("bar.sync 2, 128;" ::: "memory");
+    i8_team_sync(barrier);
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
       const int at = is_up ? kHalf + i : i;
       const float other = mail[at * 64 + row % 64];
-      const float y = is_up ? silu_mul(other, kept[i]) : silu_mul(kept[i], other);
-      if (mine && at < left) to[at * a.width] = i8_out<OUT>(y);
+      stage[at * kCh + row % 64] = i8_out<OUT>(is_up ? silu_mul(other, kept[i]) : silu_mul(kept[i], other));
+    }
+  }
+  i8_team_sync(barrier);
+  const int left = static_cast<int>(a.m - tok0 < COLS ? a.m - tok0 : COLS);
+  OUT *to = static_cast<OUT *>(a.out) + tok0 * a.width + ch0;
+  if (a.aligned) {
+#pragma unroll
+    for (int j = 0; j < COLS * kCh / kPiece / 128; ++j) {
+      const int i = (j * 128 + row) / (kCh / kPiece), c = (j * 128 + row) % (kCh / kPiece) * kPiece;
+      if (i < left && ch0 + c < a.width)
+        *reinterpret_cast<uint4 *>(to + i * a.width + c) = *reinterpret_cast<const uint4 *>(stage + i * kCh + c);
+    }
+  } else {
+    for (int j = row; j < COLS * kCh; j += 128) {
+      const int i = j / kCh, c = j % kCh;
+      if (i < left && ch0 + c < a.width) to[i * a.width + c] = stage[j];
     }
   }
 }
@@ -358,7 +406,7 @@ __device__ __forceinline__ bool i8_all_fine(bool fine, int barrier) {
         : "=r"(all)
         : "r"(fine ? 1u : 0u)
         : "memory");
-  return all != 0;
+  return __all_sync(0xFFFFFFFFu, all != 0);
 }
 
 template <typename OUT, int NT, bool PAIR, bool GATED>
@@ -369,7 +417,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   constexpr int kChannels = GATED ? 64 : 128;  // outputs' channels of a CTA's tile
   extern __shared__ char smem_raw[];
   __shared__ I8Barriers bars;
-  __shared__ float xs_of[PAIR ? 1 : NT];
+  __shared__ float xs_of[NT], ws_of[PAIR ? 1 : 128];
   const I8Args &a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR || t.split > 1 ? cluster_ctarank() : 0;
@@ -527,27 +575,20 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         if (i8_elect()) i8_commit<PAIR>(acc_full);
         __syncwarp();
         i8_wait(acc_full, acc_phase, &never, limit, status);
+      } else if (PAIR) {
+        // The other CTA's last arrivals have come before this one's memory goes.
+        i8_wait(acc_empty, acc_phase ^ 1, abort, limit, status);
       }
     }
     if (PAIR) {
-      // The last stages' slots come back too before this CTA's memory goes.
+      // So have those of the last stages' products, at both CTAs.
       for (int i = 0; i < Shape::kOps && i < total; ++i) {
         const uint32_t n = static_cast<uint32_t>(total - 1 - i);
         if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
       }
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---- scales of x for the parts' sums
-    if (!PAIR) {
-      int tn, tm;
-      place(tile0, tn, tm);
-      for (int i = threadIdx.x - 64; i < NT; i += 64) {
-        const int64_t tok = static_cast<int64_t>(tm) * NT + i;
-        xs_of[PAIR ? 0 : i] = tok < a.m ? __ldg(a.xs + tok) : 0.f;
-      }
-    }
-  } else if (warp < Shape::kOutWarp0) {
+  } else if (warp >= 4 && warp < Shape::kOutWarp0) {
     // ---- operands: a team takes every kTeams-th stage; a thread unpacks a row
     // of w, and a row of x or a part of one (the lanes of a group of eight take
     // the same bytes of eight rows).
@@ -627,16 +668,14 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       int tn, tm;
       place(tile0, tn, tm);
       const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-      const int64_t ch = static_cast<int64_t>(tn) * kChannels + (GATED ? at % 64 : at);
+      const int64_t ch0 = static_cast<int64_t>(tn) * kChannels, ch = ch0 + (GATED ? at % 64 : at);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
-      float ws = 0.f, xs[NT / 16];
-      if (t.split == 1) {
-        ws = ch < a.width ? __ldg(a.ws + ch + (GATED && at >= 64 ? a.width : 0)) : 0.f;
-#pragma unroll
-        for (int c = 0; c < NT / 16; ++c)
-          xs[c] = lane < 16 && tok + c * 16 + lane < a.m ? __ldg(a.xs + tok + c * 16 + lane) : 0.f;
-      }
-      if (i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), 1 + team)) {
+      const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && at >= 64 ? a.width : 0)) : 0.f;
+      ws_of[PAIR ? 0 : at] = ws;  // each team the same
+      if (at < NT) xs_of[at] = tok + at < a.m ? __ldg(a.xs + tok + at) : 0.f;
+      const bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), 1 + team);
+      if (t.split > 1) i8_cluster_arrive();  // this CTA's rings are free
+      if (fine) {
         i8_fence_after();
 #pragma unroll
         for (int c = 0; c < NT / 16; ++c) {
@@ -644,35 +683,37 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           uint32_t v[16];
           i8_tmem_load16(acc + c * 16, v);
           if (t.split == 1) {
-            float *mail = ring + (team * 2 + c / Shape::kTeams % 2) * (16 * 64);
-            i8_write<OUT, GATED, 16>(a, v, ws, xs[c], tok + c * 16, ch, at, mail, 1 + team);
+            char *buf = reinterpret_cast<char *>(ring) +
+                        (team * 2 + c / Shape::kTeams % 2) * Shape::kBuffer;
+            i8_write<OUT, GATED, 16>(a, v, ws, xs_of + c * 16, tok + c * 16, ch0, at, buf,
+                                     1 + team);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               ring[(c * 16 + i) * kI8TileRows + at] = __uint_as_float(v[i]);
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (t.split > 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
     }
-  } else if constexpr (PAIR) {
+  } else if (PAIR && warp >= Shape::kOutWarp0) {
     // ---- outputs of a pair's tile
     const int row = (warp & 3) * 32 + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t leader_empty = i8_mapa(acc_empty, 0);
-    float *mail = ring + Shape::kRings / 4;
+    char *buf = reinterpret_cast<char *>(ring) + Shape::kRings;
     uint32_t acc_phase = 0;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
-      const int64_t ch = static_cast<int64_t>(tn * 2 + static_cast<int>(rank)) * kChannels +
-                         (GATED ? row % 64 : row);
+      const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(rank)) * kChannels;
+      const int64_t ch = ch0 + (GATED ? row % 64 : row);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
       const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
-      float xs[NT / 32];
+      i8_team_sync(1);  // the last tile's scales have been read
 #pragma unroll
-      for (int c = 0; c < NT / 32; ++c)
-        xs[c] = tok + c * 32 + lane < a.m ? __ldg(a.xs + tok + c * 32 + lane) : 0.f;
+      for (int i = 0; i < NT; i += 128)
+        xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
       if (!i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 1)) break;
       acc_phase ^= 1;
       i8_fence_after();
@@ -685,7 +726,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           __syncwarp();
           if (lane == 0) i8_arrive_cluster(leader_empty);
         }
-        i8_write<OUT, GATED, 32>(a, v, ws, xs[c], tok + c * 32, ch, row, mail + (c & 1) * (32 * 64), 1);
+        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + c * 32, tok + c * 32, ch0, row,
+                                 buf + (c & 1) * Shape::kBuffer, 1);
       }
     }
   }
@@ -700,34 +742,59 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       const uint32_t share = static_cast<uint32_t>(cols) * kI8TileRows * 4;
       const uint32_t inbox = base + NT * kI8TileRows * 4, parts = smem_addr(&bars.parts);
       if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars.parts, S * share);
-      int tn, tm;
-      place(tile0, tn, tm);
-      const int l = threadIdx.x % kChannels;
-      const int64_t ch = static_cast<int64_t>(tn) * kChannels + l;
-      const int64_t tok0 = static_cast<int64_t>(tm) * NT + rank * cols;
-      const float ws = ch < a.width ? __ldg(a.ws + ch) : 0.f;
-      const float ws_up = GATED && ch < a.width ? __ldg(a.ws + ch + a.width) : 0.f;
-      cluster_arrive_release();  // the rings of all are free, the parts written
-      cluster_wait_acquire();
+      if (warp < 4) i8_cluster_arrive();
+      i8_cluster_wait();  // the rings of all are free
+      __syncthreads();    // the parts are written
       if (threadIdx.x < S && !*abort)
         asm volatile(
             "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
             ::"r"(i8_mapa(inbox + rank * share, threadIdx.x)), "r"(base + threadIdx.x * share), "r"(share),
             "r"(i8_mapa(parts, threadIdx.x))
             : "memory");
+      int tn, tm;
+      place(tile0, tn, tm);
+      const int64_t ch0 = static_cast<int64_t>(tn) * kChannels;
+      const int64_t tok0 = static_cast<int64_t>(tm) * NT + rank * cols;
       if (i8_wait(parts, 0, abort, limit, status)) {
-        const float *from = ring + NT * kI8TileRows + l;
-        OUT *out = static_cast<OUT *>(a.out);
-        for (int col = threadIdx.x / kChannels; col < cols; col += Shape::kThreads / kChannels) {
-          float y = 0.f, up = 0.f;
-          for (int p = 0; p < S; ++p) {
-            y += from[(p * cols + col) * kI8TileRows];
-            if (GATED) up += from[(p * cols + col) * kI8TileRows + 64];
+        constexpr int kPiece = 16 / sizeof(OUT), kPieces = kChannels / kPiece;
+        for (int i = threadIdx.x; i < cols * kPieces; i += Shape::kThreads) {
+          const int col = i / kPieces, l = i % kPieces * kPiece;
+          const float *from = ring + (NT + col) * kI8TileRows + l;
+          float y[kPiece], up[kPiece];
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e) y[e] = up[e] = 0.f;
+          for (int p = 0; p < S; ++p, from += cols * kI8TileRows) {
+#pragma unroll
+            for (int e = 0; e < kPiece; e += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(from + e);
+              y[e] += f.x;
+              y[e + 1] += f.y;
+              y[e + 2] += f.z;
+              y[e + 3] += f.w;
+              if (GATED) {
+                const float4 g = *reinterpret_cast<const float4 *>(from + 64 + e);
+                up[e] += g.x;
+                up[e + 1] += g.y;
+                up[e + 2] += g.z;
+                up[e + 3] += g.w;
+              }
+            }
           }
           const float xs = xs_of[rank * cols + col];
-          y = y * ws * xs;
-          if (GATED) y = silu_mul(y, up * ws_up * xs);
-          if (ch < a.width && tok0 + col < a.m) out[(tok0 + col) * a.width + ch] = i8_out<OUT>(y);
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e) {
+            y[e] = y[e] * ws_of[l + e] * xs;
+            if (GATED) y[e] = silu_mul(y[e], up[e] * ws_of[64 + l + e] * xs);
+          }
+          if (tok0 + col >= a.m) continue;
+          OUT *to = static_cast<OUT *>(a.out) + (tok0 + col) * a.width + ch0 + l;
+          if (a.aligned) {
+            if (ch0 + l < a.width) *reinterpret_cast<uint4 *>(to) = i8_pack<OUT>(y);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e)
+              if (ch0 + l + e < a.width) to[e] = i8_out<OUT>(y[e]);
+          }
         }
       }
       __syncwarp();
@@ -736,8 +803,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   // Nobody leaves while its cluster may still use its memory.
   i8_fence_before();
   if (PAIR || t.split > 1) {
-    cluster_arrive_release();
-    cluster_wait_acquire();
+    i8_cluster_arrive();
+    i8_cluster_wait();
   }
   __syncthreads();
   i8_fence_after();
