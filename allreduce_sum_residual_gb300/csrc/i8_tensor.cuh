@@ -347,28 +347,33 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
   constexpr int kCh = GATED ? 64 : 128, kPiece = 16 / sizeof(OUT);
   float *mail = reinterpret_cast<float *>(buf);
   OUT *stage = reinterpret_cast<OUT *>(buf + (GATED ? COLS * 64 * 4 : 0));
+  // All loads from shared memory before any store, which might be to the same
+  // place for all that the compiler knows, and no branch between activations:
+  // one after the other they took a tile 15 us more.
+  float y[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) y[i] = __uint_as_float(v[i]) * ws * xs[i];
   if constexpr (!GATED) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) stage[i * kCh + row] = i8_out<OUT>(__uint_as_float(v[i]) * ws * xs[i]);
+    for (int i = 0; i < COLS; ++i) stage[i * kCh + row] = i8_out<OUT>(y[i]);
   } else {
     constexpr int kHalf = COLS / 2;
     const bool is_up = row >= 64;
-    float kept[kHalf];
+    const int gives = is_up ? 0 : kHalf, first = is_up ? kHalf : 0;
+    float kept[kHalf], other[kHalf];
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) {
-      const float y = __uint_as_float(v[i]) * ws * xs[i];
-      if (is_up == (i < kHalf))
-        mail[i * 64 + row % 64] = y;
-      else
-        kept[i % kHalf] = y;
+    for (int i = 0; i < kHalf; ++i) {
+      mail[(gives + i) * 64 + row % 64] = is_up ? y[i] : y[kHalf + i];
+      kept[i] = is_up ? y[kHalf + i] : y[i];
     }
     i8_team_sync(barrier);
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i) {
-      const int at = is_up ? kHalf + i : i;
-      const float other = mail[at * 64 + row % 64];
-      stage[at * kCh + row % 64] = i8_out<OUT>(is_up ? silu_mul(other, kept[i]) : silu_mul(kept[i], other));
-    }
+    for (int i = 0; i < kHalf; ++i) other[i] = mail[(first + i) * 64 + row % 64];
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+      kept[i] = silu_mul(is_up ? other[i] : kept[i], is_up ? kept[i] : other[i]);
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) stage[(first + i) * kCh + row % 64] = i8_out<OUT>(kept[i]);
   }
   i8_team_sync(barrier);
   const int left = static_cast<int>(a.m - tok0 < COLS ? a.m - tok0 : COLS);
