@@ -10,6 +10,15 @@ static cudaError_t allow_wide_clusters(BlockNormKernel kern) {
                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
+// Packs of a thread where there are rows enough for a CTA each.  A norm after the
+// block is a second sum that a row has to wait for: four packs a thread, half as
+// many warps to meet and more loads under way in each (8192 rows of 6144, one
+// partial: 60.5 us, with two packs 79 us).  Without it, and with so many
+// partials that loads are under way anyway, two packs keep more threads (4096
+// rows of 8192: four partials and the norm 69 us against 74 us, two without it
+// 59 us against 66 us).
+static int packs_a_thread(int n, bool post) { return post && n <= 3 ? 4 : 2; }
+
 static int run_block_norm(const void *const *partials, int n, int type, const void *post_weight,
                           const void *gate, int64_t gate_stride, int64_t gate_rows,
                           float block_scale, const void *residual, int residual_type,
@@ -83,22 +92,30 @@ static int run_block_norm(const void *const *partials, int n, int type, const vo
   a.status = d->status;
   // CTAs a row: as many as leave each 64 packs while the grid is below one
   // CTA an SM, up to 8; at least as many as hold the row in registers.
-  int S = 1;
+  int S = 1, vpt = 1;
   while (S < 8 && m * S * 2 <= d->sms && a.P / (S * 2) >= 64) S *= 2;
+  const bool few = S > 1;
   while ((a.P + S - 1) / S > kMaxPacksPerCta) S *= 2;
+  if (!few) vpt = S > 1 ? 4 : packs_a_thread(n, post_weight != nullptr);
   a.per_cta = (a.P + S - 1) / S;
   a.split = S;
-  const int threads = (a.per_cta + 31) / 32 * 32;
+  const int threads = ((a.per_cta + vpt - 1) / vpt + 31) / 32 * 32;
   if (m > INT32_MAX / S) return AR_ERR_UNSUPPORTED;
-  int ctas;
-  const BlockNormKernel kern = type == AR_TYPE_BF16
-                                   ? block_norm_bf16(residual_type == AR_TYPE_F32, S > 1, threads, &ctas)
-                                   : block_norm_f16(residual_type == AR_TYPE_F32, S > 1, threads, &ctas);
+  int registers;
+  const bool r32 = residual_type == AR_TYPE_F32;
+  const BlockNormKernel kern = type == AR_TYPE_BF16 ? block_norm_bf16(r32, S > 1, vpt, &registers)
+                                                    : block_norm_f16(r32, S > 1, vpt, &registers);
   if (S > 8 && allow_wide_clusters(kern) != cudaSuccess) {
     cudaGetLastError();
     return AR_ERR_CUDA;
   }
-  if (S == 1) a.ahead = static_cast<int64_t>(d->sms) * ctas;
+  if (!few) {  // a wave of CTAs, but not more rows than 26 MB of L2
+    const int by_threads = 2048 / threads, by_registers = 65536 / (registers * threads);
+    const int ctas = by_threads < by_registers ? by_threads : by_registers;
+    const int64_t wave = static_cast<int64_t>(d->sms) * (ctas > 32 ? 32 : ctas) / S;
+    const int64_t most = (int64_t{26} << 20) / (H * (2 * n + rsize));
+    a.ahead = wave < most ? wave : most;
+  }
   return launch_pdl(kern, a, m * S, threads, 0, S, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? AR_OK
              : AR_ERR_CUDA;
