@@ -8,13 +8,13 @@ struct I8Plan {
   int split;
 };
 
-static I8Plan i8_plan(int64_t m, int64_t width, int64_t K, bool gated, int sms, int pairs) {
+static I8Plan i8_plan(int64_t m, int64_t width, int64_t K, bool gated, int sms, const int *pairs) {
   if (m <= 8) return {0, 1};
   const int64_t channels = gated ? 64 : 128;
   const int64_t tiles_n = (width + channels - 1) / channels, steps = (K + 127) / 128;
   if (m > 128) {
     const int64_t tiles = (tiles_n + 1) / 2 * ((m + 255) / 256);
-    if (tiles * 4 >= pairs * 3) return {256, 1};
+    if (tiles * 4 >= pairs[0] * 3) return {256, 1};
   }
   const int tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = tiles_n * ((m + tokens - 1) / tokens);
@@ -59,14 +59,14 @@ static int run_i8_matmul(const int8_t *x, const float *x_scales, const int8_t *w
   a.gated = act == AR_ACT_SILU_MUL;
   a.out_type = out_type;
   a.status = d->status;
-  int pairs = 0;
+  const int *pairs = nullptr;
   st = ready_i8_tensor(d->sms, &pairs);
   if (st != AR_OK) return st;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   const I8Plan p = i8_plan(m, width, K, a.gated, d->sms, pairs);
   if (p.tokens == 0)
     return launch_i8_matvec(a, d->sms, on) == cudaSuccess ? AR_OK : AR_ERR_CUDA;
-  return launch_i8_tensor(a, p.tokens, p.split, pairs, on);
+  return launch_i8_tensor(a, p.tokens, p.split, pairs[0], on);
 }
 
 }  // namespace arn

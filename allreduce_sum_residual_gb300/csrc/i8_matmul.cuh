@@ -42,10 +42,10 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {
 
 cudaError_t launch_i8_matvec(I8Args a, int sms, cudaStream_t stream);
 // `tokens`: of a tile (16, 32, 64 or 128 of one CTA, 256 of a pair); `split`:
-// CTAs of one CTA's tile.  An AR_* status.
+// parts of K of a tile; `pairs`: that run at a time.  An AR_* status.
 int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStream_t stream);
-// Shared memory for the tensor kernels, once per device, and the pairs of
-// CTAs that the current device runs at a time.
-int ready_i8_tensor(int sms, int *pairs);
+// Shared memory for the tensor kernels, once per device, and the clusters of 1, 2
+// and 4 pairs that the current device runs at a time.
+int ready_i8_tensor(int sms, const int **pairs);
 
 }  // namespace arn

@@ -18,16 +18,16 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
 
 static EncodeTiled g_encode = nullptr;
 
-int ready_i8_tensor(int sms, int *pairs) {
+int ready_i8_tensor(int sms, const int **pairs) {
   static std::mutex mu;
-  static int of_device[kMaxDevices];
+  static int of_device[kMaxDevices][3];
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
     return AR_ERR_CUDA;
   }
   std::lock_guard<std::mutex> lock(mu);
-  if (of_device[dev] == 0) {
+  if (of_device[dev][0] == 0) {
     if (g_encode == nullptr) {
       void *fn = nullptr;
       cudaDriverEntryPointQueryResult found;
@@ -49,26 +49,29 @@ int ready_i8_tensor(int sms, int *pairs) {
             return AR_ERR_CUDA;
           }
         }
-    // Pairs need two SMs of one cluster of the device; some SMs may have no
-    // partner.
-    const I8Tensor k = i8_tensor(AR_TYPE_BF16, 256, false);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(k.threads), 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k.kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      return AR_ERR_CUDA;
+    // Clusters of 1, 2 and 4 pairs that the device runs at a time: some SMs
+    // have no partners left.
+    int found[3];
+    for (int i = 2; i >= 0; --i) {
+      const I8Tensor k = i8_tensor(AR_TYPE_BF16, 256, false);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>((sms >> (i + 1)) << (i + 1)), 1, 1);
+      cfg.blockDim = dim3(static_cast<unsigned>(k.threads), 1, 1);
+      cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      found[i] = 0;
+      if (cudaOccupancyMaxActiveClusters(&found[i], k.kernel, &cfg) != cudaSuccess || found[i] < 1) {
+        cudaGetLastError();
+        return AR_ERR_CUDA;
+      }
     }
-    of_device[dev] = n;
+    for (int i = 2; i >= 0; --i) of_device[dev][i] = found[i];
   }
   *pairs = of_device[dev];
   return AR_OK;
@@ -96,15 +99,15 @@ int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStre
   const int64_t tiles_n = (a.width + channels - 1) / channels, tiles_m = (a.m + tokens - 1) / tokens;
   t.tiles_n = static_cast<int>(tiles_n);
   t.tiles_m = static_cast<int>(tiles_m);
-  t.split = pair ? 1 : split;
+  t.split = split;
   t.group = 8;
   t.wait_limit_ns = kWaitLimitNs;
   const int64_t tiles = tiles_n * tiles_m;
-  int64_t grid = tiles * t.split;
-  if (pair) grid = (tiles < pairs ? tiles : pairs) * 2;
+  // Pairs without a split take tiles in turn.
+  const int64_t grid = pair ? (split > 1 || tiles < pairs ? tiles : pairs) * split * 2 : tiles * split;
   if (grid > INT32_MAX) return AR_ERR_UNSUPPORTED;
-  return launch_pdl(k.kernel, t, grid, k.threads, static_cast<size_t>(k.smem), pair ? 2 : t.split,
-                    stream) == cudaSuccess
+  return launch_pdl(k.kernel, t, grid, k.threads, static_cast<size_t>(k.smem),
+                    pair ? split * 2 : split, stream) == cudaSuccess
              ? AR_OK
              : AR_ERR_CUDA;
 }

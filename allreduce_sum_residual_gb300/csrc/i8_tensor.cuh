@@ -27,9 +27,9 @@
 // unpack a stage each in turn, and of a pair four more warps write the outputs
 // while the next tile's operands are unpacked.  Between them rings of mbarriers, every wait
 // bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA
-// takes one tile, or with few tiles a cluster of `split` CTAs takes one, each
-// a part of K, and they add the parts up through the cluster's shared memory in
-// the order of their ranks.
+// takes one tile.  With few tiles a cluster of `split` CTAs or pairs takes one,
+// each a part of K, and they add the parts up through the cluster's shared
+// memory, in a fixed order.
 #pragma once
 
 #include <cuda.h>
@@ -42,7 +42,7 @@ struct I8TensorArgs {
   CUtensorMap w_map, x_map;
   I8Args a;
   int tiles_n, tiles_m;  // tiles of channels, of tokens
-  int split;             // CTAs of a tile (one CTA a tile)
+  int split;             // parts of K, a cluster's CTAs or pairs (1: none)
   int group;             // token tiles that are walked together (pairs)
   uint64_t wait_limit_ns;
 };
@@ -60,10 +60,11 @@ struct I8Shape {
   // on a slot whose last but one load is still another team's to see would
   // take that load's phase for the one before it.  (Operand slots are given
   // back in order.)
-  static constexpr int kTeams = PAIR ? 3 : NT == 64 ? 1 : 2;
-  static constexpr int kOps = PAIR || NT <= 32 ? 3 : 2;
-  static constexpr int kRaw = PAIR ? 3 : NT == 64 ? 3 : 4;
-  static_assert(kRaw % kTeams == 0 && kTeams <= kOps, "a team's slots");
+  static constexpr int kTeams = NT >= 128 ? 3 : NT == 64 ? 1 : 2;
+  static constexpr int kOps = NT == 64 ? 2 : 3;
+  static constexpr int kRaw = NT >= 64 ? 3 : 4;
+  static_assert(kRaw % kTeams == 0 && kTeams <= kOps && kTeams <= 3, "a team's slots");
+  static_assert(kRaw <= 4 && kOps <= 3, "barriers");
   static constexpr int kOutWarp0 = 4 + 4 * kTeams;    // of a pair's warps that write
   static constexpr int kWarps = kOutWarp0 + (PAIR ? 4 : 0);
   static constexpr int kThreads = kWarps * 32;
@@ -192,14 +193,14 @@ __device__ __forceinline__ void i8_mma(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-// Arrives at `bar` (of both CTAs of a pair) once this thread's products so far
-// are done.
+// Arrives at `bar` (of both CTAs of a pair, `rank` and the next) once this
+// thread's products so far are done.
 template <bool PAIR>
-__device__ __forceinline__ void i8_commit(uint32_t bar) {
+__device__ __forceinline__ void i8_commit(uint32_t bar, uint32_t rank) {
   if constexpr (PAIR)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
+        "[%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3u << rank))
         : "memory");
   else
     asm volatile(
@@ -307,11 +308,15 @@ __device__ __forceinline__ __half i8_out<__half>(float v) {
   return __float2half_rn(v);
 }
 
-__device__ __forceinline__ void i8_team_sync(int barrier) {
-  if (barrier == 1)
+// A barrier of a team's four warps (its number in the instruction: a register
+// would count as all sixteen).
+__device__ __forceinline__ void i8_team_sync(int team) {
+  if (team == 0)
     asm volatile("bar.sync 1, 128;" ::: "memory");
-  else
+  else if (team == 1)
     asm volatile("bar.sync 2, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 3, 128;" ::: "memory");
 }
 
 // Eight, or four fp32, outputs in a row.
@@ -343,7 +348,7 @@ __device__ __forceinline__ uint4 i8_pack<__half>(const float *y) {
 template <typename OUT, bool GATED, int COLS>
 __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[COLS], float ws,
                                          const float *xs, int64_t tok0, int64_t ch0, int row, char *buf,
-                                         int barrier) {
+                                         int team) {
   constexpr int kCh = GATED ? 64 : 128, kPiece = 16 / sizeof(OUT);
   float *mail = reinterpret_cast<float *>(buf);
   OUT *stage = reinterpret_cast<OUT *>(buf + (GATED ? COLS * 64 * 4 : 0));
@@ -366,7 +371,7 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
       mail[(gives + i) * 64 + row % 64] = is_up ? y[i] : y[kHalf + i];
       kept[i] = is_up ? y[kHalf + i] : y[i];
     }
-    i8_team_sync(barrier);
+    i8_team_sync(team);
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) other[i] = mail[(first + i) * 64 + row % 64];
 #pragma unroll
@@ -375,7 +380,7 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) stage[(first + i) * kCh + row % 64] = i8_out<OUT>(kept[i]);
   }
-  i8_team_sync(barrier);
+  i8_team_sync(team);
   const int left = static_cast<int>(a.m - tok0 < COLS ? a.m - tok0 : COLS);
   OUT *to = static_cast<OUT *>(a.out) + tok0 * a.width + ch0;
   if (a.aligned) {
@@ -393,26 +398,27 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
   }
 }
 
-// Whether all of four warps are `fine` (at barrier 1 or 2): a wait that one of them gave up ends
+// Whether all of a team's warps are `fine`: a wait that one of them gave up ends
 // all their parts in the barriers behind it.
-__device__ __forceinline__ bool i8_all_fine(bool fine, int barrier) {
+#define ARN_I8_ALL_FINE(id)                                              \
+  asm volatile(                                                          \
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"               \
+      "barrier.cta.red.and.pred q, " #id ", 128, p;\n\t"                 \
+      "selp.u32 %0, 1, 0, q;\n\t}"                                       \
+      : "=r"(all)                                                        \
+      : "r"(fine ? 1u : 0u)                                              \
+      : "memory")
+__device__ __forceinline__ bool i8_all_fine(bool fine, int team) {
   uint32_t all;
-  if (barrier == 1)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(fine ? 1u : 0u)
-        : "memory");
+  if (team == 0)
+    ARN_I8_ALL_FINE(1);
+  else if (team == 1)
+    ARN_I8_ALL_FINE(2);
   else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(fine ? 1u : 0u)
-        : "memory");
+    ARN_I8_ALL_FINE(3);
   return __all_sync(0xFFFFFFFFu, all != 0);
 }
+#undef ARN_I8_ALL_FINE
 
 template <typename OUT, int NT, bool PAIR, bool GATED>
 __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>::kCtasPerSm)
@@ -426,6 +432,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   const I8Args &a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR || t.split > 1 ? cluster_ctarank() : 0;
+  const uint32_t part = rank / kGroup, half = rank % kGroup;  // of the split, of a pair
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   float *const ring = reinterpret_cast<float *>(smem_raw + (base - smem_addr(smem_raw)));
   const uint32_t ops = base + Shape::kRaw * Shape::kRawBytes;
@@ -456,12 +463,13 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
 
   // This CTA's k steps and tiles.
   const int steps = (a.K + kI8StepK - 1) / kI8StepK;
-  const int step0 = PAIR ? 0 : steps * static_cast<int>(rank) / t.split;
-  const int step1 = PAIR ? steps : steps * static_cast<int>(rank + 1) / t.split;
+  const int step0 = steps * static_cast<int>(part) / t.split;
+  const int step1 = steps * static_cast<int>(part + 1) / t.split;
   const int tiles = t.tiles_n * t.tiles_m;
-  const int tile0 = static_cast<int>(blockIdx.x) / (PAIR ? 2 : t.split);
-  const int tile_step = PAIR ? static_cast<int>(gridDim.x) / 2 : tiles;
-  const int total = (tiles - tile0 + tile_step - 1) / tile_step * (step1 - step0);  // stages
+  const int tile0 = static_cast<int>(blockIdx.x) / (kGroup * t.split);
+  const int tile_step = static_cast<int>(gridDim.x) / (kGroup * t.split);
+  const int my_tiles = (tiles - tile0 + tile_step - 1) / tile_step;
+  const int total = my_tiles * (step1 - step0);  // stages
   // Tile -> (tile of channels, tile of tokens): pairs walk `group` token tiles
   // together over all channels, whose x then stays in L2.
   auto place = [&](int tile, int &tn, int &tm) {
@@ -499,9 +507,9 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     for (int tile = tile0; fine && tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
-      const int ch = (PAIR ? tn * 2 + static_cast<int>(rank) : tn) * kChannels;
+      const int ch = (tn * kGroup + static_cast<int>(half)) * kChannels;
       const int ch2 = GATED ? static_cast<int>(a.width) + ch : ch + 64;
-      const int tok = tm * NT + (PAIR ? static_cast<int>(rank) * Shape::kTokens : 0);
+      const int tok = tm * NT + static_cast<int>(half) * Shape::kTokens;
       for (int s = step0; s < step1; ++s) {
         fine = __all_sync(0xFFFFFFFFu, i8_wait(raw_empty + r * 8, phase ^ 1, abort, limit, status));
         if (!fine) break;
@@ -534,7 +542,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     __syncwarp();
   } else if (warp == 1) {
     // ---- products
-    if (!PAIR || rank == 0) {
+    if (half == 0) {
       // Instruction descriptor: fp32 sums, fp16 operands, both along k.
       constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) |
                                  (static_cast<uint32_t>(PAIR ? 16 : 8) << 24);
@@ -563,8 +571,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
               i8_mma<PAIR>(tmem, at + ks * 8, kDesc | ((from >> 4) & 0x3FFF), idesc,
                            step > step0 || ks > 0);
             }
-            i8_commit<PAIR>(op_empty + s * 8);
-            if (step + 1 == step1) i8_commit<PAIR>(acc_full);
+            i8_commit<PAIR>(op_empty + s * 8, rank);
+            if (step + 1 == step1) i8_commit<PAIR>(acc_full, rank);
           }
           __syncwarp();
           if (++s == Shape::kOps) {
@@ -577,19 +585,9 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       if (!fine) {
         // Products in flight end before their operands go.
         int never = 0;
-        if (i8_elect()) i8_commit<PAIR>(acc_full);
+        if (i8_elect()) i8_commit<PAIR>(acc_full, rank);
         __syncwarp();
         i8_wait(acc_full, acc_phase, &never, limit, status);
-      } else if (PAIR) {
-        // The other CTA's last arrivals have come before this one's memory goes.
-        i8_wait(acc_empty, acc_phase ^ 1, abort, limit, status);
-      }
-    }
-    if (PAIR) {
-      // So have those of the last stages' products, at both CTAs.
-      for (int i = 0; i < Shape::kOps && i < total; ++i) {
-        const uint32_t n = static_cast<uint32_t>(total - 1 - i);
-        if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
       }
     }
     __syncwarp();
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     static_assert(kSets >= 1 && kSets <= 8, "threads of a row of x");
     const int row = at % Shape::kTokens, set = at / Shape::kTokens;
     const uint32_t w_swizzle = at & 7, x_swizzle = row & 7;
-    const uint32_t leader = PAIR ? i8_mapa(op_full, 0) : 0;  // the CTA that issues the products
+    const uint32_t leader = PAIR ? i8_mapa(op_full, rank & ~1u) : 0;  // the CTA that issues the products
     int r = team, s = team;
     uint32_t raw_phase = 0, op_phase = 0;
     for (int n = team; n < total; n += Shape::kTeams) {
@@ -678,7 +676,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && at >= 64 ? a.width : 0)) : 0.f;
       ws_of[PAIR ? 0 : at] = ws;  // each team the same
       if (at < NT) xs_of[at] = tok + at < a.m ? __ldg(a.xs + tok + at) : 0.f;
-      const bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), 1 + team);
+      const bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), team);
       if (t.split > 1) i8_cluster_arrive();  // this CTA's rings are free
       if (fine) {
         i8_fence_after();
@@ -690,8 +688,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           if (t.split == 1) {
             char *buf = reinterpret_cast<char *>(ring) +
                         (team * 2 + c / Shape::kTeams % 2) * Shape::kBuffer;
-            i8_write<OUT, GATED, 16>(a, v, ws, xs_of + c * 16, tok + c * 16, ch0, at, buf,
-                                     1 + team);
+            i8_write<OUT, GATED, 16>(a, v, ws, xs_of + c * 16, tok + c * 16, ch0, at, buf, team);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -702,41 +699,96 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       }
     }
   } else if (PAIR && warp >= Shape::kOutWarp0) {
-    // ---- outputs of a pair's tile
+    // ---- outputs of a pair's tile, or of a share of its tokens: each pair of a
+    // split sends the others their shares of its sums, keeps its own in tensor
+    // memory and adds what comes, in the order of the parts.
     const int row = (warp & 3) * 32 + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    const uint32_t leader_empty = i8_mapa(acc_empty, 0);
+    const uint32_t leader_empty = i8_mapa(acc_empty, rank & ~1u), parts = smem_addr(&bars.parts);
     char *buf = reinterpret_cast<char *>(ring) + Shape::kRings;
+    const int S = t.split, chunks = NT / 32 / S;  // of 32 tokens, of this CTA
+    const int share = chunks * 32 * kI8TileRows;  // floats
+    const float *inbox = ring + (S - 1) * share;
+    if (S > 1 && row == 0) mbar_arrive_expect_tx(&bars.parts, (S - 1) * share * 4);
     uint32_t acc_phase = 0;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
-      const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(rank)) * kChannels;
+      const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(half)) * kChannels;
       const int64_t ch = ch0 + (GATED ? row % 64 : row);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
       const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
-      i8_team_sync(1);  // the last tile's scales have been read
+      i8_team_sync(0);  // the last tile's scales have been read
 #pragma unroll
       for (int i = 0; i < NT; i += 128)
         xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
-      if (!i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 1)) break;
+      bool fine = i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 0);
       acc_phase ^= 1;
       i8_fence_after();
+      if (S > 1) {  // one tile a cluster
+        i8_cluster_arrive();  // this CTA's rings are free
+        for (int c = 0; fine && c < NT / 32; ++c) {
+          const int to = c / chunks;
+          if (to == static_cast<int>(part)) continue;
+          float *out = ring + (to - (to > static_cast<int>(part))) * share +
+                       (c - to * chunks) * 32 * kI8TileRows + row;
+          uint32_t v[32];
+          i8_tmem_load32(acc + c * 32, v);
 #pragma unroll
-      for (int c = 0; c < NT / 32; ++c) {
+          for (int i = 0; i < 32; ++i) out[i * kI8TileRows] = __uint_as_float(v[i]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        i8_cluster_wait();  // those of all are
+        i8_team_sync(0);
+        if (row < S - 1 && !*abort) {
+          const uint32_t to = row + (row >= static_cast<int>(part));
+          const uint32_t there = part - (part > to);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+              "[%3];" ::"r"(i8_mapa(smem_addr(inbox + there * share), to * 2 + half)),
+              "r"(smem_addr(ring + row * share)), "r"(share * 4), "r"(i8_mapa(parts, to * 2 + half))
+              : "memory");
+        }
+        __syncwarp();
+        fine = i8_all_fine(fine && i8_wait(parts, 0, abort, limit, status), 0);
+      }
+      if (!fine) break;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        const int at = static_cast<int>(part) * chunks + c;
         uint32_t v[32];
-        i8_tmem_load32(acc + c * 32, v);
-        if (c == NT / 32 - 1) {
+        i8_tmem_load32(acc + at * 32, v);
+        if (c == chunks - 1) {
           i8_fence_before();
           __syncwarp();
           if (lane == 0) i8_arrive_cluster(leader_empty);
         }
-        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + c * 32, tok + c * 32, ch0, row,
-                                 buf + (c & 1) * Shape::kBuffer, 1);
+        for (int p = 0; p < S - 1; ++p) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) +
+                                   inbox[p * share + (c * 32 + i) * kI8TileRows + row]);
+        }
+        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + at * 32, tok + at * 32, ch0, row,
+                                 buf + (c & 1) * Shape::kBuffer, 0);
       }
     }
   }
   __syncwarp();
+  if (PAIR && t.split > 1 && warp < Shape::kOutWarp0) {
+    i8_cluster_arrive();
+    i8_cluster_wait();
+  }
+  if (PAIR && warp == 1) {
+    // Every arrival at this CTA that nobody has waited for comes before its
+    // memory goes: of the last stages' products, of the last tile's readers.
+    for (int i = 0; i < Shape::kOps && i < total; ++i) {
+      const uint32_t n = static_cast<uint32_t>(total - 1 - i);
+      if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
+    }
+    if (half == 0) i8_wait(acc_empty, static_cast<uint32_t>(my_tiles - 1) & 1, abort, limit, status);
+    __syncwarp();
+  }
 
   if constexpr (!PAIR) {
     if (t.split > 1) {
