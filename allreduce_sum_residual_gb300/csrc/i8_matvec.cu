@@ -16,6 +16,10 @@ namespace arn {
 
 constexpr int kVecWarps = 8;
 constexpr int kVecRows = 4;
+// Bytes of a row, for each warp of its team, that are prefetched before the previous
+// grid's end: one token through 7168 x 7168 takes 9.1 us, 11.2 us without and
+// 11.5 us where the whole row is.
+constexpr int kVecPrefetch = 1536;
 
 __device__ __forceinline__ int4 ld_stream16(const int8_t *p) {
   int4 v;
@@ -36,8 +40,6 @@ template <int MT, bool GATED>
 __global__ void __launch_bounds__(kVecWarps * 32)
     k_i8_matvec(const __grid_constant__ I8Args a) {
   __shared__ int part[kVecWarps][kVecRows * MT];
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = warp % a.team;
   constexpr int kOuts = GATED ? kVecRows / 2 : kVecRows;
@@ -52,6 +54,18 @@ __global__ void __launch_bounds__(kVecWarps * 32)
     const int64_t j = min(j0 + (GATED ? r / 2 : r), a.width - 1) + (GATED && (r & 1) ? a.width : 0);
     wp[r] = a.w + j * a.K;
   }
+  // The first bytes of the team's rows, on their way to L2 while the previous grid
+  // ends.
+  if (sub == 0 && lane == 0 && j0 < a.width) {
+    const uint32_t bytes = static_cast<uint32_t>(min(a.K, kVecPrefetch * a.team));
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) {
+      if (in_bounds(wp[r] + a.K <= a.w + static_cast<int64_t>(a.N) * a.K, a.status))
+        prefetch_l2(wp[r], bytes);
+    }
+  }
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
 #pragma unroll
   for (int t = 0; t < MT; ++t) xp[t] = a.x + min(i0 + t, a.m - 1) * a.K;
   int acc[kVecRows][MT];
@@ -113,7 +127,8 @@ __global__ void __launch_bounds__(kVecWarps * 32)
     for (int u = 0; u < a.team; ++u) s += part[warp + u][r * MT + t];
     v[h] = static_cast<float>(s) * __ldg(a.ws + j + (h ? a.width : 0)) * xs;
   }
-  i8_store(a, i * a.width + j, GATED ? silu_mul(v[0], v[1]) : v[0]);
+  if (in_bounds(i * a.width + j < a.m * a.width && warp + a.team <= kVecWarps, a.status))
+    i8_store(a, i * a.width + j, GATED ? silu_mul(v[0], v[1]) : v[0]);
 }
 
 using MatvecKernel = void (*)(I8Args);

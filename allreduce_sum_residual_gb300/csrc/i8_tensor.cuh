@@ -50,6 +50,9 @@ struct I8TensorArgs {
 constexpr int kI8TileRows = 128;  // channels of a CTA
 constexpr int kI8StepK = 128;     // k of a stage
 constexpr int kI8RawW = kI8TileRows * kI8StepK;
+// Stages whose weights are prefetched before the previous grid's end (32 tokens, 32768
+// x 6144 gated: 35.7 us, 36.4 us without).
+constexpr int kI8Prefetch = 3;
 
 // NT: tokens of a tile; PAIR: two CTAs share it.
 template <int NT, bool PAIR>
@@ -147,6 +150,12 @@ __device__ __forceinline__ void i8_load_box(uint32_t dst, const CUtensorMap *map
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void i8_prefetch_box(const CUtensorMap *map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x),
+               "r"(y)
+               : "memory");
 }
 
 template <bool PAIR>
@@ -387,13 +396,16 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
 #pragma unroll
     for (int j = 0; j < COLS * kCh / kPiece / 128; ++j) {
       const int i = (j * 128 + row) / (kCh / kPiece), c = (j * 128 + row) % (kCh / kPiece) * kPiece;
-      if (i < left && ch0 + c < a.width)
+      if (i < left && ch0 + c < a.width &&
+          in_bounds((tok0 + i) * a.width + ch0 + c + kPiece <= a.m * a.width, a.status))
         *reinterpret_cast<uint4 *>(to + i * a.width + c) = *reinterpret_cast<const uint4 *>(stage + i * kCh + c);
     }
   } else {
     for (int j = row; j < COLS * kCh; j += 128) {
       const int i = j / kCh, c = j % kCh;
-      if (i < left && ch0 + c < a.width) to[i * a.width + c] = stage[j];
+      if (i < left && ch0 + c < a.width &&
+          in_bounds((tok0 + i) * a.width + ch0 + c < a.m * a.width, a.status))
+        to[i * a.width + c] = stage[j];
     }
   }
 }
@@ -488,6 +500,18 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   const uint32_t op_full = smem_addr(bars.op_full), op_empty = smem_addr(bars.op_empty);
   const uint32_t acc_full = smem_addr(&bars.acc_full), acc_empty = smem_addr(&bars.acc_empty);
 
+  if (warp == 0 && i8_elect()) {
+    // The first stages' weights, on their way to L2 while the previous grid ends.
+    int tn, tm;
+    place(tile0, tn, tm);
+    const int ch = (tn * kGroup + static_cast<int>(half)) * kChannels;
+    for (int s = step0; s < step1 && s < step0 + kI8Prefetch; ++s) {
+      i8_prefetch_box(&t.w_map, s * kI8StepK, ch);
+      i8_prefetch_box(&t.w_map, s * kI8StepK, GATED ? static_cast<int>(a.width) + ch : ch + 64);
+    }
+  }
+  __syncwarp();
+
   i8_fence_before();
   if (PAIR || t.split > 1) {
     cluster_arrive_release();
@@ -513,7 +537,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       for (int s = step0; s < step1; ++s) {
         fine = __all_sync(0xFFFFFFFFu, i8_wait(raw_empty + r * 8, phase ^ 1, abort, limit, status));
         if (!fine) break;
-        if (i8_elect()) {
+        // Checking build: the slot, and every stage within K.
+        if (i8_elect() && in_bounds(r >= 0 && r < Shape::kRaw && s * kI8StepK < a.K, status)) {
           const uint32_t to = base + r * Shape::kRawBytes, bar = raw_full + r * 8;
           const int k = s * kI8StepK;
           mbar_arrive_expect_tx(&bars.raw_full[r], Shape::kRawBytes);
@@ -732,6 +757,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           if (to == static_cast<int>(part)) continue;
           float *out = ring + (to - (to > static_cast<int>(part))) * share +
                        (c - to * chunks) * 32 * kI8TileRows + row;
+          if (!in_bounds(out + 31 * kI8TileRows < ring + (S - 1) * share, status)) continue;
           uint32_t v[32];
           i8_tmem_load32(acc + c * 32, v);
 #pragma unroll
@@ -843,7 +869,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
             y[e] = y[e] * ws_of[l + e] * xs;
             if (GATED) y[e] = silu_mul(y[e], up[e] * ws_of[64 + l + e] * xs);
           }
-          if (tok0 + col >= a.m) continue;
+          if (tok0 + col >= a.m || !in_bounds(col < cols && l + kPiece <= kChannels, status)) continue;
           OUT *to = static_cast<OUT *>(a.out) + (tok0 + col) * a.width + ch0 + l;
           if (a.aligned) {
             if (ch0 + l < a.width) *reinterpret_cast<uint4 *>(to) = i8_pack<OUT>(y);

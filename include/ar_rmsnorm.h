@@ -616,9 +616,11 @@ int ar_i8_quantize(const void *x, int type, int64_t row_stride, int64_t m,
 /*
  * out[i, j] = x_scales[i] * w_scales[j] * sum_k x[i, k] w[j, k], or its gated
  * half (act), rounded once to out's type.  The sum is a whole number; it is
- * exact while the sums on the way to it stay within 2^24, beyond that each is
- * rounded to fp32 at worst.  Then two fp32 products, and the activation in
- * fp32.  The pages have no counterpart of it.
+ * exact while the sums on the way to it stay within 2^24 (for any data up to K
+ * = 1024), beyond that each of them is within a step of fp32.  Then fp32
+ * products by w_scales[j] and x_scales[i], and the activation in fp32.  Equal
+ * calls give equal bits, and while the sums are exact a row's results do not
+ * depend on the batch it is in.  The pages have no counterpart of it.
  *   x         [m, K] bytes in [-128, 127].    x_scales  [m] fp32.
  *   w         [N, K] bytes in [-128, 127].    w_scales  [N] fp32.
  *   K         a multiple of 16, at most AR_I8_MAX_K.
