@@ -3,64 +3,58 @@
 
 namespace arn {
 
-struct I8Plan {
-  int tokens;  // of a tile; 0: the matvec kernel
-  int split;   // parts of K
-};
-
-// Microseconds, fitted to 1000 times of 230 shapes (1 to 2048 tokens, matrices of
-// 512 x 512 to 32768 x 6144); the choice by them is within 2 % of the best on
-// average, 14 % at most.
+// Microseconds, fitted to 2000 times of 319 shapes (1 to 2048 tokens, matrices of
+// 512 x 512 to 32768 x 6144).  The choice by them takes 0.4 % longer than the best
+// on average, 9 % at most.
 struct I8Cost {
   int tokens;
   double fixed;   // of a launch
   double join;    // each doubling of the split
-  double alone;   // a stage of 128 k of one CTA on an SM
-  double shared;  // and of each of several
+  double alone;   // a stage of 128 k of one CTA on an SM, or of a pair
+  double shared;  // and of each of several CTAs
+  double tile, gated;  // a pair's tile beside its stages
+  int splits;     // 1 to 2^(splits - 1) parts of K
 };
-constexpr I8Cost kI8Costs[] = {{16, 4.5, 0.5, 0.32, 0.32},
-                               {32, 4.6, 0.7, 0.37, 0.31},
-                               {64, 5.3, 0.9, 0.56, 0.40},
-                               {128, 4.5, 3.1, 0.60, 0.60}};
-constexpr double kI8Round = 6.8;                       // another tile behind one, one CTA a tile
-constexpr I8Cost kI8Pair = {256, 2.0, 1.6, 0.54, 0.54};
-constexpr double kI8PairTile = 6.3, kI8PairGated = 7.9;  // a pair's tile beside its stages
+constexpr I8Cost kI8Ctas[] = {{16, 4.05, 0.51, 0.37, 0.33, 0, 0, 4}, {32, 4.35, 0.64, 0.39, 0.34, 0, 0, 4}};
+constexpr double kI8Round = 5.24;  // another tile behind an SM's first two
+constexpr I8Cost kI8Pairs[] = {{64, 4.23, 0.90, 0.36, 0, 0.81, 1.33, 2},
+                               {128, 4.98, 0.65, 0.36, 0, 1.56, 2.27, 3},
+                               {256, 5.04, 1.47, 0.55, 0, 3.40, 4.98, 3}};
 
 static I8Plan i8_plan(int64_t m, int64_t width, int64_t N, int64_t K, bool gated, int sms,
                       const int *pairs) {
   const int64_t channels = gated ? 64 : 128, steps = (K + 127) / 128;
-  I8Plan best = {0, 1};
+  I8Plan best = {0, 1, false};
   double least = 1e30;
-  if (m <= 16)  // bytes a microsecond of weights, once for eight tokens
-    least = 3.2 + static_cast<double>((m + 7) / 8 * N * K) / (m <= 2 ? 6.0e6 : m <= 4 ? 4.3e6 : 2.8e6);
-  for (const I8Cost &c : kI8Costs) {
-    if (c.tokens < m && c.tokens < 128 && m > 4 * c.tokens) continue;
-    if (c.tokens >= 2 * m && c.tokens > 16) break;
+  if (m <= 16)  // bytes of weights a microsecond, once for eight tokens
+    least = 3.5 + static_cast<double>((m + 7) / 8 * N * K) /
+                      (m <= 2 ? 6.0e6 : m <= 4 ? 4.3e6 : m <= 8 ? 2.0e6 : 1.2e6);
+  for (const I8Cost &c : kI8Ctas) {
+    if (m > 4 * c.tokens || (c.tokens > 16 && c.tokens >= 2 * m)) continue;
     const int64_t tiles = (width + channels - 1) / channels * ((m + c.tokens - 1) / c.tokens);
-    const int at_a_time = c.tokens <= 64 ? 2 : 1;
-    for (int split = 1; split <= 8 && split <= steps; split *= 2) {
-      const int64_t on_sm = (tiles * split + sms - 1) / sms;
-      const double stages = static_cast<double>((steps + split - 1) / split);
-      const double t = c.fixed + (split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3) * c.join +
-                       stages * (on_sm == 1 ? c.alone : on_sm * c.shared) +
-                       static_cast<double>((on_sm - 1) / at_a_time) * kI8Round;
+    for (int i = 0; i < c.splits && (1 << i) <= steps; ++i) {
+      const int64_t on_sm = ((tiles << i) + sms - 1) / sms;
+      const double stages = static_cast<double>((steps + (1 << i) - 1) >> i);
+      const double t = c.fixed + i * c.join + stages * (on_sm == 1 ? c.alone : on_sm * c.shared) +
+                       static_cast<double>((on_sm - 1) / 2) * kI8Round;
       if (t < least) {
         least = t;
-        best = {c.tokens, split};
+        best = {c.tokens, 1 << i, false};
       }
     }
   }
-  if (m > 64) {
-    const int64_t tiles = (width + 2 * channels - 1) / (2 * channels) * ((m + 255) / 256);
-    for (int i = 0; i < 3 && (1 << i) <= steps; ++i) {
+  for (const I8Cost &c : kI8Pairs) {
+    if (m <= c.tokens / 4) break;
+    const int64_t tiles = (width + 2 * channels - 1) / (2 * channels) * ((m + c.tokens - 1) / c.tokens);
+    for (int i = 0; i < c.splits && (1 << i) <= steps; ++i) {
       if (i > 0 && tiles > pairs[i]) break;  // a split's clusters take one tile each
       const int64_t rounds = (tiles + pairs[i] - 1) / pairs[i];
       const double stages = static_cast<double>((steps + (1 << i) - 1) >> i);
-      const double t = kI8Pair.fixed + i * kI8Pair.join +
-                       rounds * (stages * kI8Pair.alone + (gated ? kI8PairGated : kI8PairTile));
+      const double t = c.fixed + i * c.join +
+                       static_cast<double>(rounds) * (stages * c.alone + (gated ? c.gated : c.tile));
       if (t < least) {
         least = t;
-        best = {256, 1 << i};
+        best = {c.tokens, 1 << i, true};
       }
     }
   }
@@ -109,7 +103,7 @@ static int run_i8_matmul(const int8_t *x, const float *x_scales, const int8_t *w
   const I8Plan p = i8_plan(m, width, N, K, a.gated, d->sms, pairs);
   if (p.tokens == 0)
     return launch_i8_matvec(a, d->sms, on) == cudaSuccess ? AR_OK : AR_ERR_CUDA;
-  return launch_i8_tensor(a, p.tokens, p.split, pairs[0], on);
+  return launch_i8_tensor(a, p, pairs[0], on);
 }
 
 }  // namespace arn

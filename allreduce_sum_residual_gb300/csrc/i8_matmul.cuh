@@ -41,9 +41,13 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {
 }
 
 cudaError_t launch_i8_matvec(I8Args a, int sms, cudaStream_t stream);
-// `tokens`: of a tile (16, 32, 64 or 128 of one CTA, 256 of a pair); `split`:
-// parts of K of a tile; `pairs`: that run at a time.  An AR_* status.
-int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStream_t stream);
+struct I8Plan {
+  int tokens;  // of a tile: 16 or 32 of one CTA, 64, 128 or 256 of a pair; 0: matvec
+  int split;   // parts of K
+  bool pair;
+};
+// `pairs`: that run at a time.  An AR_* status.
+int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream);
 // Shared memory for the tensor kernels, once per device, and the clusters of 1, 2
 // and 4 pairs that the current device runs at a time.
 int ready_i8_tensor(int sms, const int **pairs);

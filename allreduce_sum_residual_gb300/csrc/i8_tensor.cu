@@ -5,10 +5,10 @@
 
 namespace arn {
 
-static I8Tensor i8_tensor(int type, int tokens, bool gated) {
-  return type == AR_TYPE_F32    ? i8_tensor_f32(tokens, gated)
-         : type == AR_TYPE_BF16 ? i8_tensor_bf16(tokens, gated)
-                                : i8_tensor_f16(tokens, gated);
+static I8Tensor i8_tensor(int type, int tokens, bool pair, bool gated) {
+  return type == AR_TYPE_F32    ? i8_tensor_f32(tokens, pair, gated)
+         : type == AR_TYPE_BF16 ? i8_tensor_bf16(tokens, pair, gated)
+                                : i8_tensor_f16(tokens, pair, gated);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -40,20 +40,20 @@ int ready_i8_tensor(int sms, const int **pairs) {
       g_encode = reinterpret_cast<EncodeTiled>(fn);
     }
     for (int type = AR_TYPE_F32; type <= AR_TYPE_F16; ++type)
-      for (int tokens = 16; tokens <= 256; tokens *= 2)
-        for (int gated = 0; gated < 2; ++gated) {
-          const I8Tensor k = i8_tensor(type, tokens, gated != 0);
-          if (cudaFuncSetAttribute(reinterpret_cast<const void *>(k.kernel),
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
-            cudaGetLastError();
-            return AR_ERR_CUDA;
-          }
+      for (int i = 0; i < 10; ++i) {
+        const bool pair = i >= 4;  // 16 and 32 tokens of one CTA, 64 to 256 of a pair
+        const I8Tensor k = i8_tensor(type, 16 << (i / 2), pair, i % 2 != 0);
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(k.kernel),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
+          cudaGetLastError();
+          return AR_ERR_CUDA;
         }
+      }
     // Clusters of 1, 2 and 4 pairs that the device runs at a time: some SMs
     // have no partners left.
     int found[3];
     for (int i = 2; i >= 0; --i) {
-      const I8Tensor k = i8_tensor(AR_TYPE_BF16, 256, false);
+      const I8Tensor k = i8_tensor(AR_TYPE_BF16, 256, true, false);
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>((sms >> (i + 1)) << (i + 1)), 1, 1);
       cfg.blockDim = dim3(static_cast<unsigned>(k.threads), 1, 1);
@@ -87,9 +87,10 @@ static bool encode(CUtensorMap *map, const int8_t *p, int64_t K, int64_t rows, i
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_i8_tensor(const I8Args &a, int tokens, int split, int pairs, cudaStream_t stream) {
-  const I8Tensor k = i8_tensor(a.out_type, tokens, a.gated != 0);
-  const bool pair = tokens == 256;
+int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream) {
+  const int tokens = plan.tokens, split = plan.split;
+  const bool pair = plan.pair;
+  const I8Tensor k = i8_tensor(a.out_type, tokens, pair, a.gated != 0);
   I8TensorArgs t;
   t.a = a;
   t.a.aligned = aligned16(a.out) && a.width * type_size(a.out_type) % 16 == 0;

@@ -63,11 +63,11 @@ struct I8Shape {
   // on a slot whose last but one load is still another team's to see would
   // take that load's phase for the one before it.  (Operand slots are given
   // back in order.)
-  static constexpr int kTeams = NT >= 128 ? 3 : NT == 64 ? 1 : 2;
-  static constexpr int kOps = NT == 64 ? 2 : 3;
-  static constexpr int kRaw = NT >= 64 ? 3 : 4;
+  static constexpr int kTeams = PAIR ? 3 : 2;
+  static constexpr int kOps = 3;
+  static constexpr int kRaw = !PAIR ? 4 : NT <= 128 ? 6 : 3;
   static_assert(kRaw % kTeams == 0 && kTeams <= kOps && kTeams <= 3, "a team's slots");
-  static_assert(kRaw <= 4 && kOps <= 3, "barriers");
+  static_assert(kRaw <= 6 && kOps <= 3, "barriers");
   static constexpr int kOutWarp0 = 4 + 4 * kTeams;    // of a pair's warps that write
   static constexpr int kWarps = kOutWarp0 + (PAIR ? 4 : 0);
   static constexpr int kThreads = kWarps * 32;
@@ -297,7 +297,7 @@ __device__ __forceinline__ void i8_unpack(uint32_t v, uint32_t &lo, uint32_t &hi
 // --- the kernel -----------------------------------------------------------------
 
 struct I8Barriers {
-  uint64_t raw_full[4], raw_empty[4], op_full[3], op_empty[3], acc_full, acc_empty, parts;
+  uint64_t raw_full[6], raw_empty[6], op_full[3], op_empty[3], acc_full, acc_empty, parts;
   uint32_t tmem;
   int abort;
 };
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       i8_team_sync(0);  // the last tile's scales have been read
 #pragma unroll
       for (int i = 0; i < NT; i += 128)
-        xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
+        if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
       bool fine = i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 0);
       acc_phase ^= 1;
       i8_fence_after();
@@ -908,20 +908,18 @@ inline I8Tensor i8_tensor_one(bool gated) {
           Shape::kSmem, Shape::kTokens};
 }
 
-// tokens: 16, 32, 64 or 128 of one CTA, 256 of a pair.
+// tokens: 16 or 32 of one CTA, 64, 128 or 256 of a pair.
 template <typename OUT>
-inline I8Tensor i8_tensor_of(int tokens, bool gated) {
-  switch (tokens) {
-    case 16: return i8_tensor_one<OUT, 16, false>(gated);
-    case 32: return i8_tensor_one<OUT, 32, false>(gated);
-    case 64: return i8_tensor_one<OUT, 64, false>(gated);
-    case 128: return i8_tensor_one<OUT, 128, false>(gated);
-    default: return i8_tensor_one<OUT, 256, true>(gated);
-  }
+inline I8Tensor i8_tensor_of(int tokens, bool pair, bool gated) {
+  if (pair)
+    return tokens == 64    ? i8_tensor_one<OUT, 64, true>(gated)
+           : tokens == 128 ? i8_tensor_one<OUT, 128, true>(gated)
+                           : i8_tensor_one<OUT, 256, true>(gated);
+  return tokens == 16 ? i8_tensor_one<OUT, 16, false>(gated) : i8_tensor_one<OUT, 32, false>(gated);
 }
 
-I8Tensor i8_tensor_f32(int tokens, bool gated);
-I8Tensor i8_tensor_bf16(int tokens, bool gated);
-I8Tensor i8_tensor_f16(int tokens, bool gated);
+I8Tensor i8_tensor_f32(int tokens, bool pair, bool gated);
+I8Tensor i8_tensor_bf16(int tokens, bool pair, bool gated);
+I8Tensor i8_tensor_f16(int tokens, bool pair, bool gated);
 
 }  // namespace arn

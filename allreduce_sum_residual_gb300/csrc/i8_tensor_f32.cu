@@ -2,6 +2,8 @@
 
 namespace arn {
 
-I8Tensor i8_tensor_f32(int tokens, bool gated) { return i8_tensor_of<float>(tokens, gated); }
+I8Tensor i8_tensor_f32(int tokens, bool pair, bool gated) {
+  return i8_tensor_of<float>(tokens, pair, gated);
+}
 
 }  // namespace arn
