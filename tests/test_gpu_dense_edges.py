@@ -30,6 +30,21 @@ def test_a_row_does_not_depend_on_its_batch(K, N, act, dtype):
         assert torch.equal(got, want[:m]), m
 
 
+@pytest.mark.parametrize("m,K,N,act", [(5000, 4096, 4096, "none"), (3001, 5120, 5122, "silu_mul")])
+def test_a_prompt_in_two_launches(m, K, N, act):
+    """A prompt whose last tokens take a launch of their own."""
+    g = gen(m)
+    x, xs, w, ws = bytes_(g, m, K), scale(g, m), bytes_(g, N, K), scale(g, N) / 300
+    out, ok = guarded((m, N // 2 if act == "silu_mul" else N), BF)
+    arn.ar_i8_matmul(x, xs, w, ws, act=act, out=out)
+    torch.cuda.synchronize()
+    assert ok()
+    for a in range(0, m, 500):
+        assert torch.equal(out[a:a + 500], arn.ar_i8_matmul(x[a:a + 500], xs[a:a + 500], w, ws, act=act))
+    y, ey = ref.product(x[-300:], xs[-300:], w, ws, act)
+    within(out[-300:], y, ey, BF)
+
+
 @pytest.mark.parametrize("m", [2, 5, 20, 60, 140])
 @pytest.mark.parametrize("act", ["none", "silu_mul"])
 def test_longest_products(m, act):
