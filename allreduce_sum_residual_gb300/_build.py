@@ -3,7 +3,7 @@
 Each .cu file compiles to an object in parallel; the objects link into
 ``allreduce_sum_residual_gb300/libarnorm.so``.  Only nvcc is needed (no
 cmake); the same command works on x86_64 and aarch64 hosts.  Beside it g++
-builds ``_binding-<python>-<torch>.so``, the expert-layer calls on torch
+builds ``_binding-<python>-<torch>.so``, the expert layer's and the 8-bit layer's calls on torch
 tensors in one step, against the installed torch; where that cannot be built
 the library stands alone and those calls go through ctypes.
 """

@@ -49,7 +49,7 @@ static I8Plan i8_plan(int64_t m, int64_t width, int64_t N, int64_t K, bool gated
     const int64_t tiles = (width + 2 * channels - 1) / (2 * channels) * ((m + c.tokens - 1) / c.tokens);
     for (int i = 0; i < c.splits && (1 << i) <= steps; ++i) {
       if (i > 0 && tiles > pairs[i]) break;  // a split's clusters take one tile each
-      const int64_t rounds = (tiles + pairs[i] - 1) / pairs[i];
+      const int64_t rounds = i > 0 ? 1 : (tiles + pairs[0] - 1) / pairs[0];
       const double stages = static_cast<double>((steps + (1 << i) - 1) >> i);
       const double t = c.fixed + i * c.join +
                        static_cast<double>(rounds) * (stages * c.alone + (gated ? c.gated : c.tile));

@@ -10,15 +10,20 @@
 //
 // The warps of a team share a row block, each a part of K, so that short
 // matrices still give every SM its warps.
+//
+// Measured, one token: 7168 x 7168 in 9.1 us (5.7 TB/s; 3 us of it the launch and
+// the first bytes), 8192 x 1024 in 2.7 us.  With more than four tokens the dp4a are
+// the bound (some 33 lanes a clock and SM): 8 x 7168 x 7168 takes 20.7 us, on the
+// tensor cores 14.9 us.
 #include "i8_matmul.cuh"
 
 namespace arn {
 
 constexpr int kVecWarps = 8;
 constexpr int kVecRows = 4;
-// Bytes of a row, for each warp of its team, that are prefetched before the previous
-// grid's end: one token through 7168 x 7168 takes 9.1 us, 11.2 us without and
-// 11.5 us where the whole row is.
+// Bytes of a row, for each warp of its team, that are prefetched before the
+// previous grid's end: one token through 7168 x 7168 takes 9.1 us, 11.2 us without
+// and 11.5 us where the whole row is.
 constexpr int kVecPrefetch = 1536;
 
 __device__ __forceinline__ int4 ld_stream16(const int8_t *p) {

@@ -68,7 +68,8 @@ int ready_i8_tensor(int sms, const int **pairs) {
       found[i] = 0;
       if (cudaOccupancyMaxActiveClusters(&found[i], k.kernel, &cfg) != cudaSuccess || found[i] < 1) {
         cudaGetLastError();
-        return AR_ERR_CUDA;
+        if (i == 0) return AR_ERR_CUDA;
+        found[i] = 0;  // no splits into so many
       }
     }
     for (int i = 2; i >= 0; --i) of_device[dev][i] = found[i];

@@ -8,28 +8,35 @@
 // The tile.  The weights' rows are the 128 rows of the accumulator (256 of a
 // pair of CTAs, each holding its own 128), the tokens its columns.  So one
 // kernel serves from 16 tokens, where the weights' bytes are the bound and
-// each is read once, to prompts, where the tensor cores are.  Lane l of tensor
-// memory is a channel, and a warp's stores of one token are 32 channels in a
-// row.
+// each is read once, to prompts, where the tensor cores are.  A pair shares the
+// tokens' operand, each CTA unpacking half of it: above 32 tokens a CTA by itself
+// spends its time moving that operand through shared memory (128 x 7168 x 7168:
+// 23.8 us, pairs 18.8 us).
 //
 // The operands are unpacked on the way.  TMA brings boxes of 64 rows x 128
-// bytes of w and TB x 128 of x (128-byte swizzle; what lies behind the arrays'
-// ends comes as zeros, which add nothing).  Four warps turn a stage of w into
-// fp16 in tensor memory, from where the tensor core takes its A operand: a
-// thread is a row, as in tensor memory, so unpacked weights, twice the bytes,
-// never pass through shared memory.  They also turn x into the swizzled fp16
-// tile of the B operand.  A byte b becomes 1024 + (b + 128) by a byte
-// permutation under the exponent of 1024, and one half2 subtraction leaves b
-// (a published method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants
+// bytes of w and as many rows of x as the CTA has tokens (128-byte swizzle; what
+// lies behind the arrays' ends comes as zeros, which add nothing).  Four warps
+// turn a stage of w into fp16 in tensor memory, from where the tensor core takes
+// its A operand: a thread is a row, as in tensor memory, so unpacked weights,
+// twice the bytes, never pass through shared memory.  They also turn x into the
+// swizzled fp16 tile of the B operand.  A byte b becomes 1024 + (b + 128) by a
+// byte permutation under the exponent of 1024, and one half2 subtraction leaves
+// b (a published method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants
 // Can't Run", 2022).
 //
-// Roles: a thread issues the loads, a thread the products, teams of four warps
-// unpack a stage each in turn, and of a pair four more warps write the outputs
-// while the next tile's operands are unpacked.  Between them rings of mbarriers, every wait
-// bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA
-// takes one tile.  With few tiles a cluster of `split` CTAs or pairs takes one,
-// each a part of K, and they add the parts up through the cluster's shared
-// memory, in a fixed order.
+// Roles: a warp issues the loads, a warp the products, teams of four warps unpack
+// a stage each in turn, and of a pair four more warps write the outputs while the
+// next tile's operands are unpacked.  Between them rings of mbarriers, every wait
+// bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA takes
+// one tile.  With few tiles a cluster of `split` CTAs or pairs takes one, each a
+// part of K, and they add the parts up through the cluster's shared memory, in a
+// fixed order.
+//
+// Measured: 8192 x 6144 x 8192 in 422 us, 1955 TFLOP/s (a library's bf16 product
+// of that rate: 1933); a stage of 128 k of a full pair takes 1030 clocks, 1024 of
+// them the tensor core's, and shared memory is in use for as many: 32 KB in, out,
+// unpacked and read again.  16 x 6144 x 32768 gated in 35.3 us, 5.7 TB/s: memory,
+// and 256 tiles on 152 SMs.
 #pragma once
 
 #include <cuda.h>
@@ -50,8 +57,8 @@ struct I8TensorArgs {
 constexpr int kI8TileRows = 128;  // channels of a CTA
 constexpr int kI8StepK = 128;     // k of a stage
 constexpr int kI8RawW = kI8TileRows * kI8StepK;
-// Stages whose weights are prefetched before the previous grid's end (32 tokens, 32768
-// x 6144 gated: 35.7 us, 36.4 us without).
+// Stages whose weights are prefetched before the previous grid's end (32 tokens,
+// 32768 x 6144 gated: 35.7 us, 36.4 us without).
 constexpr int kI8Prefetch = 3;
 
 // NT: tokens of a tile; PAIR: two CTAs share it.
@@ -324,9 +331,13 @@ __device__ __forceinline__ void i8_team_sync(int team) {
     asm volatile("bar.sync 1, 128;" ::: "memory");
   else if (team == 1)
     asm volatile("bar.sync 2, 128;" ::: "memory");
-  else
+  else if (team == 2)
     asm volatile("bar.sync 3, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 4, 128;" ::: "memory");
 }
+// Of all warps but the first four of a pair's CTA.
+__device__ __forceinline__ void i8_teams_sync() { asm volatile("bar.sync 5, 512;" ::: "memory"); }
 
 // Eight, or four fp32, outputs in a row.
 template <typename OUT>
@@ -426,8 +437,10 @@ __device__ __forceinline__ bool i8_all_fine(bool fine, int team) {
     ARN_I8_ALL_FINE(1);
   else if (team == 1)
     ARN_I8_ALL_FINE(2);
-  else
+  else if (team == 2)
     ARN_I8_ALL_FINE(3);
+  else
+    ARN_I8_ALL_FINE(4);
   return __all_sync(0xFFFFFFFFu, all != 0);
 }
 #undef ARN_I8_ALL_FINE
@@ -724,19 +737,13 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       }
     }
   } else if (PAIR && warp >= Shape::kOutWarp0) {
-    // ---- outputs of a pair's tile, or of a share of its tokens: each pair of a
-    // split sends the others their shares of its sums, keeps its own in tensor
-    // memory and adds what comes, in the order of the parts.
+    // ---- outputs of a pair's tiles
     const int row = (warp & 3) * 32 + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    const uint32_t leader_empty = i8_mapa(acc_empty, rank & ~1u), parts = smem_addr(&bars.parts);
+    const uint32_t leader_empty = i8_mapa(acc_empty, rank & ~1u);
     char *buf = reinterpret_cast<char *>(ring) + Shape::kRings;
-    const int S = t.split, chunks = NT / 32 / S;  // of 32 tokens, of this CTA
-    const int share = chunks * 32 * kI8TileRows;  // floats
-    const float *inbox = ring + (S - 1) * share;
-    if (S > 1 && row == 0) mbar_arrive_expect_tx(&bars.parts, (S - 1) * share * 4);
     uint32_t acc_phase = 0;
-    for (int tile = tile0; tile < tiles; tile += tile_step) {
+    for (int tile = tile0; t.split == 1 && tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
       const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(half)) * kChannels;
@@ -747,63 +754,101 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
 #pragma unroll
       for (int i = 0; i < NT; i += 128)
         if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
-      bool fine = i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 0);
+      if (!i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 0)) break;
       acc_phase ^= 1;
       i8_fence_after();
-      if (S > 1) {  // one tile a cluster
-        i8_cluster_arrive();  // this CTA's rings are free
-        for (int c = 0; fine && c < NT / 32; ++c) {
-          const int to = c / chunks;
-          if (to == static_cast<int>(part)) continue;
-          float *out = ring + (to - (to > static_cast<int>(part))) * share +
-                       (c - to * chunks) * 32 * kI8TileRows + row;
-          if (!in_bounds(out + 31 * kI8TileRows < ring + (S - 1) * share, status)) continue;
-          uint32_t v[32];
-          i8_tmem_load32(acc + c * 32, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) out[i * kI8TileRows] = __uint_as_float(v[i]);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        i8_cluster_wait();  // those of all are
-        i8_team_sync(0);
-        if (row < S - 1 && !*abort) {
-          const uint32_t to = row + (row >= static_cast<int>(part));
-          const uint32_t there = part - (part > to);
-          asm volatile(
-              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-              "[%3];" ::"r"(i8_mapa(smem_addr(inbox + there * share), to * 2 + half)),
-              "r"(smem_addr(ring + row * share)), "r"(share * 4), "r"(i8_mapa(parts, to * 2 + half))
-              : "memory");
-        }
-        __syncwarp();
-        fine = i8_all_fine(fine && i8_wait(parts, 0, abort, limit, status), 0);
-      }
-      if (!fine) break;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int at = static_cast<int>(part) * chunks + c;
+      for (int c = 0; c < NT / 32; ++c) {
         uint32_t v[32];
-        i8_tmem_load32(acc + at * 32, v);
-        if (c == chunks - 1) {
+        i8_tmem_load32(acc + c * 32, v);
+        if (c == NT / 32 - 1) {
           i8_fence_before();
           __syncwarp();
           if (lane == 0) i8_arrive_cluster(leader_empty);
         }
-        for (int p = 0; p < S - 1; ++p) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(__uint_as_float(v[i]) +
-                                   inbox[p * share + (c * 32 + i) * kI8TileRows + row]);
-        }
-        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + at * 32, tok + at * 32, ch0, row,
+        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + c * 32, tok + c * 32, ch0, row,
                                  buf + (c & 1) * Shape::kBuffer, 0);
       }
     }
   }
   __syncwarp();
-  if (PAIR && t.split > 1 && warp < Shape::kOutWarp0) {
-    i8_cluster_arrive();
-    i8_cluster_wait();
+  if (PAIR && t.split > 1) {
+    if (warp < 4) {
+      i8_cluster_arrive();
+      i8_cluster_wait();
+    } else {
+      // ---- outputs of a share of a tile's tokens: each pair of a split sends the
+      // others their shares of its sums, keeps its own in tensor memory and adds
+      // what comes, in the order of the parts.  All teams take part, 32 tokens
+      // each in turn.
+      constexpr int kGroups = Shape::kTeams + 1;
+      static_assert(!PAIR || kGroups == 4, "i8_teams_sync");
+      static_assert(!PAIR || NT < 256 || 2 * (NT / 2) * kI8TileRows * 4 + 2 * Shape::kBuffer <= Shape::kRings,
+                    "buffers behind a split's sums");
+      const int g = (warp - 4) / 4, row = (warp & 3) * 32 + lane;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21), parts = smem_addr(&bars.parts);
+      const int S = t.split, chunks = NT / 32 / S;  // of 32 tokens, of this CTA
+      const int share = chunks * 32 * kI8TileRows;  // floats
+      const float *inbox = ring + (S - 1) * share;
+      int tn, tm;
+      place(tile0, tn, tm);
+      const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(half)) * kChannels;
+      const int64_t ch = ch0 + (GATED ? row % 64 : row);
+      const int64_t tok = static_cast<int64_t>(tm) * NT;
+      const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; i += 128)  // each team the same
+        if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
+      if (g == 0 && row == 0) mbar_arrive_expect_tx(&bars.parts, (S - 1) * share * 4);
+      bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), g);
+      i8_fence_after();
+      i8_cluster_arrive();  // this CTA's rings are free
+      for (int c = g; fine && c < NT / 32; c += kGroups) {
+        const int to = c / chunks;
+        if (to == static_cast<int>(part)) continue;
+        float *out = ring + (to - (to > static_cast<int>(part))) * share +
+                     (c - to * chunks) * 32 * kI8TileRows + row;
+        if (!in_bounds(out + 31 * kI8TileRows < ring + (S - 1) * share, status)) continue;
+        uint32_t v[32];
+        i8_tmem_load32(acc + c * 32, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) out[i * kI8TileRows] = __uint_as_float(v[i]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      i8_cluster_wait();  // those of all are
+      i8_teams_sync();    // the sums to send are written
+      if (g == 0 && row < S - 1 && !*abort) {
+        const uint32_t to = row + (row >= static_cast<int>(part));
+        const uint32_t there = part - (part > to);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+            ::"r"(i8_mapa(smem_addr(inbox + there * share), to * 2 + half)),
+            "r"(smem_addr(ring + row * share)), "r"(share * 4), "r"(i8_mapa(parts, to * 2 + half))
+            : "memory");
+      }
+      __syncwarp();
+      if (g < chunks) {
+        fine = i8_all_fine(fine && i8_wait(parts, 0, abort, limit, status), g);
+        if (fine) {
+          const int at = static_cast<int>(part) * chunks + g;
+          uint32_t v[32];
+          i8_tmem_load32(acc + at * 32, v);
+          for (int p = 0; p < S - 1; ++p) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(__uint_as_float(v[i]) +
+                                     inbox[p * share + (g * 32 + i) * kI8TileRows + row]);
+          }
+          char *buf = reinterpret_cast<char *>(ring) +
+                      (g < 2 ? Shape::kRings + g * Shape::kBuffer
+                             : 2 * (S - 1) * share * 4 + (g - 2) * Shape::kBuffer);
+          i8_write<OUT, GATED, 32>(a, v, ws, xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
+        }
+      } else {
+        i8_wait(parts, 0, abort, limit, status);
+      }
+      __syncwarp();
+    }
   }
   if (PAIR && warp == 1) {
     // Every arrival at this CTA that nobody has waited for comes before its
@@ -812,7 +857,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       const uint32_t n = static_cast<uint32_t>(total - 1 - i);
       if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
     }
-    if (half == 0) i8_wait(acc_empty, static_cast<uint32_t>(my_tiles - 1) & 1, abort, limit, status);
+    if (half == 0 && t.split == 1)
+      i8_wait(acc_empty, static_cast<uint32_t>(my_tiles - 1) & 1, abort, limit, status);
     __syncwarp();
   }
 
