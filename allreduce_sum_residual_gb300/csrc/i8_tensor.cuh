@@ -11,7 +11,7 @@
 // each is read once, to prompts, where the tensor cores are.  A pair shares the
 // tokens' operand, each CTA unpacking half of it: above 32 tokens a CTA by itself
 // spends its time moving that operand through shared memory (128 x 7168 x 7168:
-// 23.8 us, pairs 18.8 us).
+// 23.8 us, pairs 17.3 us).
 //
 // The operands are unpacked on the way.  TMA brings boxes of 64 rows x 128
 // bytes of w and as many rows of x as the CTA has tokens (128-byte swizzle; what
@@ -91,7 +91,7 @@ struct I8Shape {
   static constexpr int kSmem = 1024 + kRings + kExchange;
   static constexpr int kCtasPerSm = kCols == 256 && kSmem <= 113 * 1024 ? 2 : 1;
   static_assert(PAIR || 2 * NT * kI8TileRows * 4 <= kRings, "the parts of a tile fit the rings");
-  static_assert(kSmem + NT * 4 + (PAIR ? 0 : 512) + 256 <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kSmem + NT * 4 + 512 + 256 <= 227 * 1024, "shared memory of a CTA");
   static_assert(kAccCols + kOps * kOpCols <= 512, "tensor memory");
   // CTAs that fit an SM's shared memory together never ask for more tensor
   // memory than it has, whichever of these kernels they are of: an allocation
@@ -358,6 +358,35 @@ __device__ __forceinline__ uint4 i8_pack<__half>(const float *y) {
   return pack16<__half>(f);
 }
 
+// Rows that begin anywhere: `room` channels, at most kCh, of `left` tokens from
+// `stage` to `to`, element by element; nothing at or behind `end`.
+template <typename OUT, int kCh, int COLS>
+__device__ __forceinline__ void i8_copy_out(OUT *to, const OUT *stage, int64_t width, int left, int64_t room,
+                                            const OUT *end, int row, int *status) {
+  const int c = row % kCh;
+#pragma unroll 1
+  for (int j0 = 0; j0 < COLS * kCh / 128; j0 += 8) {
+    OUT y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = stage[(j0 + j) * 128 + row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = ((j0 + j) * 128 + row) / kCh;
+      if (i < left && c < room && in_bounds(to + i * width + c < end, status)) to[i * width + c] = y[j];
+    }
+  }
+}
+
+// The same as a call: in the loop over a pair's tiles, where nothing else waits for
+// the writing warps, inlined it took 2048 x 4096 x 2001 from 26.9 us to 35, the
+// products waiting with it.  Elsewhere the call costs more than it saves
+// (40 x 4112 x 1001 on one CTA a tile: 15.6 us, inlined 15.3).
+template <typename OUT, int kCh, int COLS>
+__device__ __noinline__ void i8_copy_out_call(OUT *to, const OUT *stage, int64_t width, int left, int64_t room,
+                                              const OUT *end, int row, int *status) {
+  i8_copy_out<OUT, kCh, COLS>(to, stage, width, left, room, end, row, status);
+}
+
 // Writes COLS tokens of a tile's channels from the sums: four warps, a thread
 // a channel (`row` of the tile, scale `ws`), tokens tok0 .. of the output with
 // the scales xs[0 ..].  The outputs pass through shared memory, `buf` (two
@@ -412,12 +441,11 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
         *reinterpret_cast<uint4 *>(to + i * a.width + c) = *reinterpret_cast<const uint4 *>(stage + i * kCh + c);
     }
   } else {
-    for (int j = row; j < COLS * kCh; j += 128) {
-      const int i = j / kCh, c = j % kCh;
-      if (i < left && ch0 + c < a.width &&
-          in_bounds((tok0 + i) * a.width + ch0 + c < a.m * a.width, a.status))
-        to[i * a.width + c] = stage[j];
-    }
+    const OUT *end = static_cast<const OUT *>(a.out) + a.m * a.width;
+    if constexpr (COLS == 32 && !GATED)
+      i8_copy_out_call<OUT, kCh, COLS>(to, stage, a.width, left, a.width - ch0, end, row, a.status);
+    else
+      i8_copy_out<OUT, kCh, COLS>(to, stage, a.width, left, a.width - ch0, end, row, a.status);
   }
 }
 
@@ -453,7 +481,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   constexpr int kChannels = GATED ? 64 : 128;  // outputs' channels of a CTA's tile
   extern __shared__ char smem_raw[];
   __shared__ I8Barriers bars;
-  __shared__ float xs_of[NT], ws_of[PAIR ? 1 : 128];
+  __shared__ float xs_of[NT], ws_of[128];
   const I8Args &a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR || t.split > 1 ? cluster_ctarank() : 0;
@@ -712,7 +740,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       const int64_t ch0 = static_cast<int64_t>(tn) * kChannels, ch = ch0 + (GATED ? at % 64 : at);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
       const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && at >= 64 ? a.width : 0)) : 0.f;
-      ws_of[PAIR ? 0 : at] = ws;  // each team the same
+      ws_of[at] = ws;  // each team the same
       if (at < NT) xs_of[at] = tok + at < a.m ? __ldg(a.xs + tok + at) : 0.f;
       const bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), team);
       if (t.split > 1) i8_cluster_arrive();  // this CTA's rings are free
@@ -795,10 +823,12 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(half)) * kChannels;
       const int64_t ch = ch0 + (GATED ? row % 64 : row);
       const int64_t tok = static_cast<int64_t>(tm) * NT;
-      const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
+      if (g == kGroups - 1) {  // idle until now: the others would wait for these
+        ws_of[row] = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
 #pragma unroll
-      for (int i = 0; i < NT; i += 128)  // each team the same
-        if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
+        for (int i = 0; i < NT; i += 128)
+          if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
+      }
       if (g == 0 && row == 0) mbar_arrive_expect_tx(&bars.parts, (S - 1) * share * 4);
       bool fine = i8_all_fine(i8_wait(acc_full, 0, abort, limit, status), g);
       i8_fence_after();
@@ -816,7 +846,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       i8_cluster_wait();  // those of all are
-      i8_teams_sync();    // the sums to send are written
+      i8_teams_sync();    // the sums to send are written, and the scales
       if (g == 0 && row < S - 1 && !*abort) {
         const uint32_t to = row + (row >= static_cast<int>(part));
         const uint32_t there = part - (part > to);
@@ -842,10 +872,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           char *buf = reinterpret_cast<char *>(ring) +
                       (g < 2 ? Shape::kRings + g * Shape::kBuffer
                              : 2 * (S - 1) * share * 4 + (g - 2) * Shape::kBuffer);
-          i8_write<OUT, GATED, 32>(a, v, ws, xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
+          i8_write<OUT, GATED, 32>(a, v, ws_of[row], xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
         }
-      } else {
-        i8_wait(parts, 0, abort, limit, status);
       }
       __syncwarp();
     }
