@@ -26,8 +26,8 @@
 //
 // Roles: a warp issues the loads, a warp the products, teams of four warps unpack
 // a stage each in turn, and of a pair four more warps write the outputs while the
-// next tile's operands are unpacked.  Between them rings of mbarriers, every wait
-// bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA takes
+// next tile's operands are unpacked, gated with the teams' help.  Between them rings
+// of mbarriers, every wait bounded.  A pair of CTAs is persistent and takes tiles in turn; one CTA takes
 // one tile.  With few tiles a cluster of `split` CTAs or pairs takes one, each a
 // part of K, and they add the parts up through the cluster's shared memory, in a
 // fixed order.
@@ -394,7 +394,7 @@ __device__ __noinline__ void i8_copy_out_call(OUT *to, const OUT *stage, int64_t
 // (as 2 bytes a lane they took three times as long).  Gated, rows 0..63 are the
 // gates of rows 64..127: they give the later half of the tokens away and take
 // the other rows' earlier half, and every thread computes half.
-template <typename OUT, bool GATED, int COLS>
+template <typename OUT, bool GATED, int COLS, bool PAIR>
 __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[COLS], float ws,
                                          const float *xs, int64_t tok0, int64_t ch0, int row, char *buf,
                                          int team) {
@@ -442,7 +442,7 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
     }
   } else {
     const OUT *end = static_cast<const OUT *>(a.out) + a.m * a.width;
-    if constexpr (COLS == 32 && !GATED)
+    if constexpr (PAIR && !GATED)
       i8_copy_out_call<OUT, kCh, COLS>(to, stage, a.width, left, a.width - ch0, end, row, a.status);
     else
       i8_copy_out<OUT, kCh, COLS>(to, stage, a.width, left, a.width - ch0, end, row, a.status);
@@ -479,6 +479,9 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   using Shape = I8Shape<NT, PAIR>;
   constexpr int kGroup = PAIR ? 2 : 1;
   constexpr int kChannels = GATED ? 64 : 128;  // outputs' channels of a CTA's tile
+  constexpr int kGroups = Shape::kTeams + 1;   // of four warps, of a pair's CTA
+  constexpr bool kAllWrite = PAIR && GATED;    // groups that write a tile: write_tile
+  constexpr int kWriters = kAllWrite ? kGroups : 1;
   extern __shared__ char smem_raw[];
   __shared__ I8Barriers bars;
   __shared__ float xs_of[NT], ws_of[128];
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       mbar_init(&bars.op_empty[i], 1);
     }
     mbar_init(&bars.acc_full, 1);
-    mbar_init(&bars.acc_empty, 4 * kGroup);
+    mbar_init(&bars.acc_empty, 4 * kWriters * kGroup);
     mbar_init(&bars.parts, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -563,6 +566,50 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   const uint32_t tmem = bars.tmem;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+
+  // The outputs of a pair's k-th tile, by group g.  Gated by all groups, a quarter of
+  // the tokens each: the tensor cores wait until the sums have been read, and activations
+  // take long (1792 x 4096 x 8192: 70.0 us, by the last group alone 72.9; 256 x 4096 x
+  // 2002: 25.4 and 27.1).  Else by the last group: by all, rows of any width would wait
+  // for one another's stores (8192 x 1024 x 4001: 68.8 us, by all 75.0; whole pieces
+  // would gain, 2048 x 4096 x 2000: 25.5, by all 24.8).  False, for all of a group,
+  // where a wait gave up or one was not `fine`.
+  auto write_tile = [&](int k, int g, bool fine) -> bool {
+    constexpr int kShare = NT / kWriters, kCols = kAllWrite ? 16 : 32;
+    static_assert(!PAIR || kShare % kCols == 0, "whole chunks");
+    int tn, tm;
+    place(tile0 + k * tile_step, tn, tm);
+    const int row = (warp & 3) * 32 + lane, first = kAllWrite ? g * kShare : 0;
+    const int64_t ch0 = static_cast<int64_t>(tn * kGroup + static_cast<int>(half)) * kChannels;
+    const int64_t ch = ch0 + (GATED ? row % 64 : row);
+    const int64_t tok = static_cast<int64_t>(tm) * NT + first;
+    const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kShare; i += 128)
+      if (i + row < kShare) xs_of[first + i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
+    if (!i8_all_fine(fine && i8_wait(acc_full, static_cast<uint32_t>(k) & 1, abort, limit, status), g))
+      return false;
+    i8_fence_after();
+    const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21) + first;
+    // Gated, a group's chunks meet twice and need one buffer.
+    char *buf = reinterpret_cast<char *>(ring) + Shape::kRings + (kAllWrite ? g * Shape::kBuffer / 2 : 0);
+#pragma unroll 1
+    for (int c = 0; c < kShare; c += kCols) {
+      uint32_t v[kCols];
+      if constexpr (kAllWrite)
+        i8_tmem_load16(acc + c, v);
+      else
+        i8_tmem_load32(acc + c, v);
+      if (c + kCols == kShare) {
+        i8_fence_before();
+        __syncwarp();
+        if (lane == 0) i8_arrive_cluster(i8_mapa(acc_empty, rank & ~1u));
+      }
+      i8_write<OUT, GATED, kCols, true>(a, v, ws, xs_of + first + c, tok + c, ch0, row,
+                                        buf + (kAllWrite ? 0 : c / kCols % 2 * Shape::kBuffer), g);
+    }
+    return true;
+  };
 
   if (warp == 0) {
     // ---- loads
@@ -657,7 +704,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < Shape::kOutWarp0) {
+  } else if (warp >= 4 && (kAllWrite || warp < Shape::kOutWarp0)) {
     // ---- operands: a team takes every kTeams-th stage; a thread unpacks a row
     // of w, and a row of x or a part of one (the lanes of a group of eight take
     // the same bytes of eight rows).
@@ -671,8 +718,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     const uint32_t leader = PAIR ? i8_mapa(op_full, rank & ~1u) : 0;  // the CTA that issues the products
     int r = team, s = team;
     uint32_t raw_phase = 0, op_phase = 0;
-    for (int n = team; n < total; n += Shape::kTeams) {
-      if (!__all_sync(0xFFFFFFFFu, i8_wait(raw_full + r * 8, raw_phase, abort, limit, status))) break;
+    auto unpack = [&]() -> bool {
+      if (!__all_sync(0xFFFFFFFFu, i8_wait(raw_full + r * 8, raw_phase, abort, limit, status))) return false;
       uint4 v[8], x[kChunks];
       const uint32_t raw = base + r * Shape::kRawBytes;
 #pragma unroll
@@ -682,7 +729,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         x[c] = i8_lds(raw + kI8RawW + row * kI8StepK + (((set * kChunks + c) ^ x_swizzle) << 4));
       __syncwarp();
       if (lane == 0) i8_arrive(raw_empty + r * 8);
-      if (!__all_sync(0xFFFFFFFFu, i8_wait(op_empty + s * 8, op_phase ^ 1, abort, limit, status))) break;
+      if (!__all_sync(0xFFFFFFFFu, i8_wait(op_empty + s * 8, op_phase ^ 1, abort, limit, status))) return false;
       i8_fence_after();
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -729,6 +776,24 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         s -= Shape::kOps;
         op_phase ^= 1;
       }
+      return true;
+    };
+    if constexpr (!kAllWrite) {
+      for (int n = team; n < total; n += Shape::kTeams)
+        if (!unpack()) break;
+    } else {
+      // A tile is written behind the team's first stage of the next, which waits for
+      // nothing but stages of tiles before; the last team only writes.  A warp whose
+      // wait gave up goes on to its team's next tile, where the others learn of it.
+      const int each = step1 - step0, to_write = t.split == 1 ? my_tiles : 0;
+      bool fine = true;
+      int n = team < Shape::kTeams ? team : total;
+      for (int k = 0; k < to_write || (t.split > 1 && fine && n < total); n += Shape::kTeams) {
+        if (fine && n < total) fine = unpack();
+        bool all = true;
+        while (all && k < to_write && (n >= total || n >= (k + 1) * each)) all = write_tile(k++, team, fine);
+        if (!all) break;
+      }
     }
     __syncwarp();
     if constexpr (!PAIR) {
@@ -754,7 +819,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           if (t.split == 1) {
             char *buf = reinterpret_cast<char *>(ring) +
                         (team * 2 + c / Shape::kTeams % 2) * Shape::kBuffer;
-            i8_write<OUT, GATED, 16>(a, v, ws, xs_of + c * 16, tok + c * 16, ch0, at, buf, team);
+            i8_write<OUT, GATED, 16, false>(a, v, ws, xs_of + c * 16, tok + c * 16, ch0, at, buf, team);
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -764,40 +829,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         if (t.split > 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
     }
-  } else if (PAIR && warp >= Shape::kOutWarp0) {
-    // ---- outputs of a pair's tiles
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-    const uint32_t leader_empty = i8_mapa(acc_empty, rank & ~1u);
-    char *buf = reinterpret_cast<char *>(ring) + Shape::kRings;
-    uint32_t acc_phase = 0;
-    for (int tile = tile0; t.split == 1 && tile < tiles; tile += tile_step) {
-      int tn, tm;
-      place(tile, tn, tm);
-      const int64_t ch0 = static_cast<int64_t>(tn * 2 + static_cast<int>(half)) * kChannels;
-      const int64_t ch = ch0 + (GATED ? row % 64 : row);
-      const int64_t tok = static_cast<int64_t>(tm) * NT;
-      const float ws = ch < a.width ? __ldg(a.ws + ch + (GATED && row >= 64 ? a.width : 0)) : 0.f;
-      i8_team_sync(0);  // the last tile's scales have been read
-#pragma unroll
-      for (int i = 0; i < NT; i += 128)
-        if (i + row < NT) xs_of[i + row] = tok + i + row < a.m ? __ldg(a.xs + tok + i + row) : 0.f;
-      if (!i8_all_fine(i8_wait(acc_full, acc_phase, abort, limit, status), 0)) break;
-      acc_phase ^= 1;
-      i8_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < NT / 32; ++c) {
-        uint32_t v[32];
-        i8_tmem_load32(acc + c * 32, v);
-        if (c == NT / 32 - 1) {
-          i8_fence_before();
-          __syncwarp();
-          if (lane == 0) i8_arrive_cluster(leader_empty);
-        }
-        i8_write<OUT, GATED, 32>(a, v, ws, xs_of + c * 32, tok + c * 32, ch0, row,
-                                 buf + (c & 1) * Shape::kBuffer, 0);
-      }
-    }
+  } else if (PAIR && !kAllWrite && warp >= Shape::kOutWarp0 && t.split == 1) {
+    for (int k = 0; k < my_tiles && write_tile(k, kGroups - 1, true);) ++k;
   }
   __syncwarp();
   if (PAIR && t.split > 1) {
@@ -809,7 +842,6 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
       // others their shares of its sums, keeps its own in tensor memory and adds
       // what comes, in the order of the parts.  All teams take part, 32 tokens
       // each in turn.
-      constexpr int kGroups = Shape::kTeams + 1;
       static_assert(!PAIR || kGroups == 4, "i8_teams_sync");
       static_assert(!PAIR || NT < 256 || 2 * (NT / 2) * kI8TileRows * 4 + 2 * Shape::kBuffer <= Shape::kRings,
                     "buffers behind a split's sums");
@@ -872,7 +904,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           char *buf = reinterpret_cast<char *>(ring) +
                       (g < 2 ? Shape::kRings + g * Shape::kBuffer
                              : 2 * (S - 1) * share * 4 + (g - 2) * Shape::kBuffer);
-          i8_write<OUT, GATED, 32>(a, v, ws_of[row], xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
+          i8_write<OUT, GATED, 32, true>(a, v, ws_of[row], xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
         }
       }
       __syncwarp();
