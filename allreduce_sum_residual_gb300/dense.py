@@ -90,7 +90,7 @@ def ar_block_rmsnorm(partials, residual, weight, eps, post_weight=None, gate=Non
     partials: n [m, H] bfloat16 or float16, rank order = reduce order.
     residual: [m, H] of their type or float32, as residual_out.  weight,
     post_weight: [H]; weight_offset is added to both in fp32.  gate: [H], or
-    [g, H] whose g rows (of any stride) share the m rows evenly, in order."""
+    [g, H] whose g rows (whole 16 bytes apart) share the m rows evenly, in order."""
     if stream is None:
         r = _fast().block_rmsnorm(partials, residual, weight, eps, post_weight, gate, block_scale,
                                   residual_scale, weight_offset, False, out, None, residual_out)

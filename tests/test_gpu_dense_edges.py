@@ -45,6 +45,16 @@ def test_a_prompt_in_two_launches(m, K, N, act):
     within(out[-300:], y, ey, BF)
 
 
+@pytest.mark.parametrize("K", [16, 128, 144, 384, 400, 528])
+@pytest.mark.parametrize("N,act", [(20011, "none"), (20016, "none"), (20012, "silu_mul"), (20016, "silu_mul")])
+def test_many_tiles_of_few_stages(K, N, act):
+    """One to five stages a tile, and several tiles for each pair of CTAs."""
+    m = 1500
+    g = gen(K + N)
+    x, xs, w, ws = bytes_(g, m, K), scale(g, m) / (4 * K ** 0.5), bytes_(g, N, K), scale(g, N)
+    check_product(x, xs, w, ws, act, [BF, F32, HF][K // 16 % 3])
+
+
 @pytest.mark.parametrize("m", [2, 5, 20, 60, 140])
 @pytest.mark.parametrize("act", ["none", "silu_mul"])
 def test_longest_products(m, act):
