@@ -1,8 +1,8 @@
 // The calls of the expert layer and of a dense layer in 8 bits on torch tensors
-// in one step, for the modules experts.py and dense.py: checks, outputs, stream and the C call, without a Python
-// statement or a ctypes conversion in between.  A decode step makes some five
-// of these calls a layer, whose kernels take 2 us each where a call through
-// ctypes takes the host 13 to 17 us.
+// in one step, for the modules experts.py and dense.py: checks, outputs, stream
+// and the C call, without a Python statement or a ctypes conversion in between.
+// A decode step makes some five of these calls a layer, whose kernels take 2 us
+// each where a call through ctypes takes the host 13 to 17 us.
 //
 // A function returns None for whatever it does not take: a wrong argument, a
 // tensor of another device than the current one, a call that the library
