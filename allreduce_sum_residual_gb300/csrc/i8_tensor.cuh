@@ -578,6 +578,9 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   auto write_tile = [&](int k, int g, bool fine) -> bool {
     constexpr int kShare = NT / kWriters, kCols = kAllWrite ? 16 : 32;
     static_assert(!PAIR || kShare % kCols == 0, "whole chunks");
+    static_assert(!kAllWrite || (kGroups * Shape::kBuffer / 2 <= Shape::kExchange &&
+                                 16 * 64 * (4 + static_cast<int>(sizeof(OUT))) <= Shape::kBuffer / 2),
+                  "a buffer for each group");
     int tn, tm;
     place(tile0 + k * tile_step, tn, tm);
     const int row = (warp & 3) * 32 + lane, first = kAllWrite ? g * kShare : 0;
