@@ -544,7 +544,7 @@ int ar_combine_rmsnorm(const void *y, int64_t rows, const int32_t *slots,
  * and the options.  Inference only.
  * --------------------------------------------------------------------------- */
 
-#define AR_I8_MAX_K    131056     /* longest dot product: sums stay below 2^31 */
+#define AR_I8_MAX_K    131056     /* longest product: its sum fits an int32    */
 #define AR_I8_MAX_N    1048576    /* rows of one 8-bit matrix                  */
 #define AR_I8_MAX_ROWS 4194304    /* tokens of one ar_i8_matmul                */
 
@@ -615,12 +615,21 @@ int ar_i8_quantize(const void *x, int type, int64_t row_stride, int64_t m,
 
 /*
  * out[i, j] = x_scales[i] * w_scales[j] * sum_k x[i, k] w[j, k], or its gated
- * half (act), rounded once to out's type.  The sum is a whole number; it is
- * exact while the sums on the way to it stay within 2^24 (for any data up to K
- * = 1024), beyond that each of them is within a step of fp32.  Then fp32
- * products by w_scales[j] and x_scales[i], and the activation in fp32.  Equal
- * calls give equal bits, and while the sums are exact a row's results do not
- * depend on the batch it is in.  The pages have no counterpart of it.
+ * half (act), rounded once to out's type.  The sum is a whole number; then come
+ * fp32 products by w_scales[j] and x_scales[i], and the activation in fp32.  The
+ * pages have no counterpart of it.
+ *
+ * The sum is taken to fp32 with one rounding, and a row's results do not depend
+ * on the batch it is in, while the sums on the way to it stay within 2^24: for
+ * any data up to K = 1024, and at any K for data whose products have both signs
+ * (a sum of K of them grows with the root of K).  Beyond that it is so for m <= 2
+ * alone.  With more rows the sum is kept in fp32, to which 16 products at a time
+ * are added, each time within a step (2^-23 of the sum): what comes out is off by
+ * at most K / 16 + 8 steps of the largest sum on the way, however small the last
+ * one is, and by how much may depend on m.  Where the operands' biases make such
+ * sums, take them out of the bytes, or give AR_ACT_NONE parts of K and add the
+ * outputs.  Equal calls give equal bits whatever the data.
+ *
  *   x         [m, K] bytes in [-128, 127].    x_scales  [m] fp32.
  *   w         [N, K] bytes in [-128, 127].    w_scales  [N] fp32.
  *   K         a multiple of 16, at most AR_I8_MAX_K.
