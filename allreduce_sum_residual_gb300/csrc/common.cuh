@@ -193,8 +193,10 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
 // Split cluster barrier.  arrive.release at kernel start (after this CTA
 // has initialised what its peers will touch), wait.acquire right before the
 // first access to a peer's shared memory -- which must not happen before
-// every CTA of the cluster runs.
+// every CTA of the cluster runs.  The instructions take whole warps: lanes that
+// a branch has parted (the one that initialises) meet first.
 __device__ __forceinline__ void cluster_arrive_release() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 

@@ -293,6 +293,7 @@ __device__ __forceinline__ bool i8_elect() {
 // have waited for is ordered by it: with a release an arrival waits for the
 // thread's stores to memory, 2000 clocks.
 __device__ __forceinline__ void i8_cluster_arrive() {
+  __syncwarp();  // it takes whole warps
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void i8_cluster_wait() {
@@ -456,6 +457,7 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
     else
       i8_copy_out<OUT, kCh, COLS>(to, stage, a.width, left, a.width - ch0, end, row, a.status);
   }
+  __syncwarp();  // behind stores that lanes skip: what comes next takes whole warps
 }
 
 // Whether all of a team's warps are `fine`: a wait that one of them gave up ends
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         i8_fence_before();
         __syncwarp();
         if (lane == 0) i8_arrive_cluster(i8_mapa(acc_empty, rank & ~1u));
+        __syncwarp();
       }
       i8_write<OUT, GATED, kCols, true>(a, v, ws, xs_of + first + c, tok + c, ch0, row,
                                         buf + (kAllWrite ? 0 : c / kCols % 2 * Shape::kBuffer), g);
