@@ -31,7 +31,8 @@ Names follow the C ABI:
     ar_i8_quantize(x) -> (q, scales)
     ar_i8_matmul(x, x_scales, w, w_scales, act="none", dtype=torch.bfloat16) -> out
     ar_device_status(device, reset),
-    ar_selftest_bounded_wait(device, limit_us), ar_strerror(status), ar_version()
+    ar_selftest_bounded_wait(device, limit_us), ar_selftest_i8_waits(device, limit_us),
+    ar_strerror(status), ar_version()
 """
 import ctypes
 import os
@@ -118,6 +119,7 @@ _SIGS = {
                                                    ctypes.c_float, _I64, _I64, _VP, _VP, _VP]),
     "ar_device_status": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "ar_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint]),
+    "ar_selftest_i8_waits": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint]),
     "ar_signal_post": (ctypes.c_int, [ctypes.POINTER(_VP), ctypes.c_int, ctypes.c_int,
                                       ctypes.c_uint32, _VP]),
     "ar_signal_wait": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint, _VP]),
@@ -508,6 +510,12 @@ def ar_device_status(device=0, reset=False):
 def ar_selftest_bounded_wait(device=0, limit_us=1000):
     """Run the bounded-wait self-test kernel; returns the status it left."""
     return int(lib().ar_selftest_bounded_wait(int(device), int(limit_us)))
+
+
+def ar_selftest_i8_waits(device=0, limit_us=1000):
+    """Run the 8-bit products' tensor-core kernels with waits that run out; the
+    status: AR_OK where each gave up with AR_ERR_TIMEOUT and left nothing behind."""
+    return int(lib().ar_selftest_i8_waits(int(device), int(limit_us)))
 
 
 # ---------------------------------------------------------------- cross-rank data plane

@@ -46,8 +46,17 @@ struct I8Plan {
   int split;   // parts of K
   bool pair;
 };
+// How long the tensor kernels' waits may take before they give up, and after that
+// those for what is still under way to a CTA; for the self-test a rank of the
+// cluster (-1: all) that loads no more than so many stages.
+constexpr int kI8AllStages = 1 << 20;  // more than AR_I8_MAX_K has
+struct I8Waits {
+  uint64_t limit_ns, settle_ns;
+  int stop_rank, stop_after;
+};
 // `pairs`: that run at a time.  An AR_* status.
-int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream);
+int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream,
+                     const I8Waits *waits = nullptr);
 // Shared memory for the tensor kernels, once per device, and the clusters of 1, 2
 // and 4 pairs that the current device runs at a time.
 int ready_i8_tensor(int sms, const int **pairs);

@@ -1,4 +1,6 @@
 // The tensor-core products' tensor maps and launches (i8_tensor.cuh).
+#include <cstdlib>
+#include <cstring>
 #include <mutex>
 
 #include "i8_tensor.cuh"
@@ -88,7 +90,8 @@ static bool encode(CUtensorMap *map, const int8_t *p, int64_t K, int64_t rows, i
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream) {
+int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_t stream,
+                     const I8Waits *waits) {
   const int tokens = plan.tokens, split = plan.split;
   const bool pair = plan.pair;
   const I8Tensor k = i8_tensor(a.out_type, tokens, pair, a.gated != 0);
@@ -103,7 +106,7 @@ int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_
   t.tiles_m = static_cast<int>(tiles_m);
   t.split = split;
   t.group = 8;
-  t.wait_limit_ns = kWaitLimitNs;
+  t.waits = waits != nullptr ? *waits : I8Waits{kWaitLimitNs, kWaitLimitNs, -1, kI8AllStages};
   const int64_t tiles = tiles_n * tiles_m;
   // Pairs without a split take tiles in turn.
   const int64_t grid = pair ? (split > 1 || tiles < pairs ? tiles : pairs) * split * 2 : tiles * split;
@@ -115,3 +118,112 @@ int launch_i8_tensor(const I8Args &a, const I8Plan &plan, int pairs, cudaStream_
 }
 
 }  // namespace arn
+
+using namespace arn;
+
+namespace {
+
+// Memory of the self-test, freed with it.
+struct TestArray {
+  void *p = nullptr;
+  ~TestArray() {
+    if (p) cudaFree(p);
+  }
+  bool make(size_t bytes, const void *from) {
+    return cudaMalloc(&p, bytes) == cudaSuccess &&
+           cudaMemcpy(p, from, bytes, cudaMemcpyHostToDevice) == cudaSuccess;
+  }
+};
+
+constexpr int kTestM = 300, kTestN = 600, kTestK = 4096, kTestOuts = kTestM * kTestN;
+
+// One shape: its outputs, then a run for each way of stopping, each followed by
+// a run that has to give the same outputs again.  An AR_* status.
+int selftest_shape(const I8Args &a, const I8Plan &plan, int device, const I8Waits &waits, float *want,
+                   float *got) {
+  const size_t bytes = static_cast<size_t>(kTestM) * a.width * sizeof(float);
+  int st = launch_i8_tensor(a, plan, 1, nullptr);  // one pair takes all tiles
+  if (st == AR_OK && cudaMemcpy(want, a.out, bytes, cudaMemcpyDeviceToHost) != cudaSuccess) st = AR_ERR_CUDA;
+  if (st != AR_OK) return st;
+  const int ranks = plan.split * (plan.pair ? 2 : 1);
+  for (int rank = -1; rank < ranks; ++rank)
+    for (int after = 0; after <= 2; after += 2) {
+      I8Waits w = waits;
+      w.stop_rank = rank;
+      w.stop_after = after;
+      st = launch_i8_tensor(a, plan, 1, nullptr, &w);
+      if (st != AR_OK) return st;
+      st = ar_device_status(device, 1);
+      if (st != AR_ERR_TIMEOUT) return st == AR_OK ? AR_ERR_CUDA : st;
+      st = launch_i8_tensor(a, plan, 1, nullptr);
+      if (st == AR_OK && cudaMemcpy(got, a.out, bytes, cudaMemcpyDeviceToHost) != cudaSuccess)
+        st = AR_ERR_CUDA;
+      if (st == AR_OK) st = ar_device_status(device, 0);
+      if (st == AR_OK && std::memcmp(want, got, bytes) != 0) st = AR_ERR_CUDA;
+      if (st != AR_OK) return st;
+    }
+  return AR_OK;
+}
+
+int selftest_waits(int device, uint64_t limit_ns, int8_t *bytes, float *want, float *got) {
+  int st = AR_OK;
+  DeviceState *d = current_device(&st);
+  const int *pairs = nullptr;
+  if (d) st = ready_i8_tensor(d->sms, &pairs);
+  if (st == AR_OK) st = ar_device_status(device, 0);
+  if (st != AR_OK) return st;
+  for (int i = 0; i < kTestN * kTestK; ++i) bytes[i] = static_cast<int8_t>(i % 251 * 37 % 255 - 127);
+  for (int i = 0; i < kTestN; ++i) want[i] = 0.001f * static_cast<float>(1 + i % 7);
+  TestArray x, xs, w, ws, out;
+  if (!x.make(kTestM * kTestK, bytes) || !w.make(kTestN * kTestK, bytes) || !xs.make(kTestM * 4, want) ||
+      !ws.make(kTestN * 4, want) || !out.make(kTestOuts * 4, want))
+    return AR_ERR_CUDA;
+  I8Args a = {};
+  a.x = static_cast<const int8_t *>(x.p);
+  a.xs = static_cast<const float *>(xs.p);
+  a.w = static_cast<const int8_t *>(w.p);
+  a.ws = static_cast<const float *>(ws.p);
+  a.out = out.p;
+  a.m = kTestM;
+  a.N = kTestN;
+  a.K = kTestK;
+  a.out_type = AR_TYPE_F32;
+  a.status = d->status;
+  const I8Waits waits = {limit_ns, 10 * limit_ns, -1, 0};
+  const I8Plan plans[] = {{16, 1, false}, {16, 4, false}, {32, 1, false}, {32, 8, false}, {64, 1, true},
+                          {64, 2, true},  {128, 1, true}, {128, 4, true}, {256, 1, true}, {256, 4, true}};
+  for (const I8Plan &p : plans) {
+    if (p.pair && p.split > 1 && pairs[p.split == 2 ? 1 : 2] == 0) continue;  // such clusters do not fit
+    for (a.gated = 0; a.gated < 2; ++a.gated) {
+      a.width = a.gated ? kTestN / 2 : kTestN;
+      st = selftest_shape(a, p, device, waits, want, got);
+      if (st != AR_OK) return st;
+    }
+  }
+  return AR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ar_selftest_i8_waits(int device, unsigned limit_us) {
+  if (device < 0 || device >= kMaxDevices || limit_us == 0 || limit_us > 100000u) return AR_ERR_ARG;
+  int prev = -1;
+  if (cudaGetDevice(&prev) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) {
+    cudaGetLastError();
+    return AR_ERR_CUDA;
+  }
+  int8_t *bytes = static_cast<int8_t *>(std::malloc(kTestN * kTestK));
+  float *outs = static_cast<float *>(std::calloc(2 * kTestOuts, sizeof(float)));
+  const int st = bytes != nullptr && outs != nullptr
+                     ? selftest_waits(device, static_cast<uint64_t>(limit_us) * 1000u, bytes, outs, outs + kTestOuts)
+                     : AR_ERR_CUDA;
+  std::free(bytes);
+  std::free(outs);
+  if (st == AR_ERR_CUDA) cudaGetLastError();
+  cudaSetDevice(prev);
+  return st;
+}
+
+}  // extern "C"

@@ -60,7 +60,7 @@ struct I8TensorArgs {
   int tiles_n, tiles_m;  // tiles of channels, of tokens
   int split;             // parts of K, a cluster's CTAs or pairs (1: none)
   int group;             // token tiles that are walked together (pairs)
-  uint64_t wait_limit_ns;
+  I8Waits waits;
 };
 
 constexpr int kI8TileRows = 128;  // channels of a CTA
@@ -233,6 +233,16 @@ __device__ __forceinline__ void i8_commit(uint32_t bar, uint32_t rank) {
         : "memory");
 }
 
+// At a barrier of this CTA alone.
+template <bool PAIR>
+__device__ __forceinline__ void i8_commit_here(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+  else
+    i8_commit<false>(bar, 0);
+}
+
 __device__ __forceinline__ void i8_tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -314,7 +324,7 @@ __device__ __forceinline__ void i8_unpack(uint32_t v, uint32_t &lo, uint32_t &hi
 // --- the kernel -----------------------------------------------------------------
 
 struct I8Barriers {
-  uint64_t raw_full[6], raw_empty[6], op_full[3], op_empty[3], acc_full, acc_empty, parts;
+  uint64_t raw_full[6], raw_empty[6], op_full[3], op_empty[3], acc_full, acc_empty, parts, quiet;
   uint32_t tmem;
   int abort;
 };
@@ -460,6 +470,15 @@ __device__ __forceinline__ void i8_write(const I8Args &a, const uint32_t (&v)[CO
   __syncwarp();  // behind stores that lanes skip: what comes next takes whole warps
 }
 
+// Where a wait gave up, before the cluster's last barrier: what its other CTAs send here
+// lands first, parts (at `parts`, if any), which they send whether this CTA gave up or
+// not, and arrivals that nobody waits for any more.
+static __device__ __noinline__ void i8_settle(uint32_t parts, uint64_t settle_ns, int *status) {
+  int never = 0;
+  if (parts != 0) i8_wait(parts, 0, &never, settle_ns, status);
+  __nanosleep(20000);
+}
+
 // Whether all of a team's warps are `fine`: a wait that one of them gave up ends
 // all their parts in the barriers behind it.
 #define ARN_I8_ALL_FINE(id)                                              \
@@ -505,7 +524,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
   const uint32_t ops = base + Shape::kRaw * Shape::kRawBytes;
   volatile int *abort = &bars.abort;
   int *status = a.status;
-  const uint64_t limit = t.wait_limit_ns;
+  const uint64_t limit = t.waits.limit_ns;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < Shape::kRaw; ++i) {
@@ -519,6 +538,7 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     mbar_init(&bars.acc_full, 1);
     mbar_init(&bars.acc_empty, 4 * kWriters * kGroup);
     mbar_init(&bars.parts, 1);
+    mbar_init(&bars.quiet, 1);
     bars.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&t.w_map) : "memory");
@@ -631,13 +651,16 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
     int r = 0, issued = 0;
     uint32_t phase = 0;
     bool fine = true;
+    int end = step1;  // (a self-test stops a CTA before)
+    if (t.waits.stop_rank < 0 || t.waits.stop_rank == static_cast<int>(rank))
+      end = min(step1, step0 + t.waits.stop_after);
     for (int tile = tile0; fine && tile < tiles; tile += tile_step) {
       int tn, tm;
       place(tile, tn, tm);
       const int ch = (tn * kGroup + static_cast<int>(half)) * kChannels;
       const int ch2 = GATED ? static_cast<int>(a.width) + ch : ch + 64;
       const int tok = tm * NT + static_cast<int>(half) * Shape::kTokens;
-      for (int s = step0; s < step1; ++s) {
+      for (int s = step0; s < end; ++s) {
         fine = __all_sync(0xFFFFFFFFu, i8_wait(raw_empty + r * 8, phase ^ 1, abort, limit, status));
         if (!fine) break;
         // Checking build: the slot, and every stage within K.
@@ -655,17 +678,17 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           phase ^= 1;
         }
       }
+      if (end < step1) break;
     }
-    if (!fine) {
-      // Loads in flight land before this CTA's memory goes.
-      int never = 0;
-      for (int i = 0; i < issued; ++i) {
-        if (--r < 0) {
-          r = Shape::kRaw - 1;
-          phase ^= 1;
-        }
-        i8_wait(raw_full + r * 8, phase, &never, limit, status);
+    // Loads in flight land before this CTA's memory goes, whoever has given up.
+    int never = 0;
+#pragma unroll 1
+    for (int i = 0; i < issued; ++i) {
+      if (--r < 0) {
+        r = Shape::kRaw - 1;
+        phase ^= 1;
       }
+      i8_wait(raw_full + r * 8, phase, &never, t.waits.settle_ns, status);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -710,13 +733,12 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
         }
         if (fine) acc_phase ^= 1;
       }
-      if (!fine) {
-        // Products in flight end before their operands go.
-        int never = 0;
-        if (i8_elect()) i8_commit<PAIR>(acc_full, rank);
-        __syncwarp();
-        i8_wait(acc_full, acc_phase, &never, limit, status);
-      }
+      // Products in flight end before their operands and their sums go, whoever has
+      // given up.
+      int never = 0;
+      if (i8_elect()) i8_commit_here<PAIR>(smem_addr(&bars.quiet));
+      __syncwarp();
+      i8_wait(smem_addr(&bars.quiet), 0, &never, t.waits.settle_ns, status);
     }
     __syncwarp();
   } else if (warp >= 4 && (kAllWrite || warp < Shape::kOutWarp0)) {
@@ -922,18 +944,21 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
           i8_write<OUT, GATED, 32, true>(a, v, ws_of[row], xs_of + at * 32, tok + at * 32, ch0, row, buf, g);
         }
       }
+      if (!fine) i8_settle(parts, t.waits.settle_ns, status);
       __syncwarp();
     }
   }
   if (PAIR && warp == 1) {
     // Every arrival at this CTA that nobody has waited for comes before its
     // memory goes: of the last stages' products, of the last tile's readers.
-    for (int i = 0; i < Shape::kOps && i < total; ++i) {
+    bool came = true;
+    for (int i = 0; came && i < Shape::kOps && i < total; ++i) {
       const uint32_t n = static_cast<uint32_t>(total - 1 - i);
-      if (!i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status)) break;
+      came = i8_wait(op_empty + n % Shape::kOps * 8, n / Shape::kOps & 1, abort, limit, status);
     }
-    if (half == 0 && t.split == 1)
-      i8_wait(acc_empty, static_cast<uint32_t>(my_tiles - 1) & 1, abort, limit, status);
+    if (came && half == 0 && t.split == 1)
+      came = i8_wait(acc_empty, static_cast<uint32_t>(my_tiles - 1) & 1, abort, limit, status);
+    if (!came) i8_settle(0, t.waits.settle_ns, status);
     __syncwarp();
   }
 
@@ -1000,6 +1025,8 @@ __global__ void __launch_bounds__(I8Shape<NT, PAIR>::kThreads, I8Shape<NT, PAIR>
               if (ch0 + l + e < a.width) to[e] = i8_out<OUT>(y[e]);
           }
         }
+      } else {
+        i8_settle(parts, t.waits.settle_ns, status);
       }
       __syncwarp();
     }

@@ -861,6 +861,19 @@ int ar_device_status(int device, int reset);
 int ar_selftest_bounded_wait(int device, unsigned limit_us);
 
 /*
+ * On `device`, run every launch shape of ar_i8_matmul's tensor-core kernels with
+ * one CTA of a cluster, and with all of them, whose loads stop before the first
+ * or the third stage, so that the waits behind them give up after limit_us
+ * microseconds (1 .. 100000); each run has to end with AR_ERR_TIMEOUT in the
+ * status word, which is cleared, and the same shape run in full after it has to
+ * give the outputs that it gave before.  AR_OK where all of that holds,
+ * AR_ERR_CUDA where not, or the status that the device held before.  Checks the
+ * kernels' ways out without faulting or hanging the GPU.  Allocates, and
+ * synchronises the device.  Library utility (no passage of the pages defines it).
+ */
+int ar_selftest_i8_waits(int device, unsigned limit_us);
+
+/*
  * 1 in the checking build (compiled with AR_CHECK=1: every kernel tests the
  * indices it derives from its launch shape before use, records
  * AR_ERR_BOUNDS in the status word and skips the access when one fails),
