@@ -306,6 +306,15 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   // In bytes.  A row whose norm holds anything that is not finite gets zeros
   // and a scale of NaN.
   if constexpr (kLate) load(wv, a.w);
+  if (!(ss < INFINITY)) {
+    // Squares past fp32's end: the norm of finite values is 0, and their product
+    // with the weight may pass the end too.
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[v][e] = 0.f * acc[v][e];
+    }
+  }
   uint32_t top = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -325,17 +334,18 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   const bool fine = top < kInfinityBits && magnitude_bits(scale) < kInfinityBits;
   // 2^100 keeps the quotient finite for rows of tiny values.
   const float up = most < 0x1p-100f ? 0x1p100f : 1.f;
-  const float by = fine && top != 0 ? 127.f / (most * up) : 0.f;
+  const bool some = fine && scale != 0.f;
+  const float by = some ? 127.f / (most * up) : 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = c0 + T0 + v * step;
     float b[8];
-    if (fine && up == 1.f) {
+    if (some && up == 1.f) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) b[e] = fmaf(acc[v][e], by, kRoundingBias);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = fmaf(fine ? acc[v][e] * up : 0.f, by, kRoundingBias);
+      for (int e = 0; e < 8; ++e) b[e] = fmaf(some ? acc[v][e] * up : 0.f, by, kRoundingBias);
     }
     if (c < end)
       __stcs(static_cast<uint2 *>(a.out) + base + c, make_uint2(bytes_of_biased(b[0], b[1], b[2], b[3]),
