@@ -3,9 +3,9 @@
 
 namespace arn {
 
-// Microseconds, fitted to 2000 times of 319 shapes (1 to 2048 tokens, matrices of
-// 512 x 512 to 32768 x 6144).  The choice by them takes 0.3 % longer than the best
-// on average, 13 % at most (0.7 us).
+// Microseconds, fitted to the times of every shape of 341 products (1 to 2048
+// tokens, matrices of 512 x 512 to 32768 x 6144), which profiles/ holds.  The choice
+// by them takes 0.4 % longer than the best on average, 13 % at most (0.7 us).
 struct I8Cost {
   int tokens;
   double fixed;   // of a launch
@@ -27,11 +27,17 @@ static I8Plan i8_plan(int64_t m, int64_t width, int64_t N, int64_t K, bool gated
   const int64_t channels = gated ? 64 : 128, steps = (K + 127) / 128;
   I8Plan best = {0, 1, false};
   double least = 1e30;
-  if (m <= 16)  // bytes of weights a microsecond, once for eight tokens
-    least = 3.5 + static_cast<double>((m + 7) / 8 * N * K) /
-                      (m <= 2 ? 7.0e6 : m <= 4 ? 4.3e6 : m <= 8 ? 2.0e6 : 1.2e6);
-  // Two tokens at most never go faster on the tensor cores (one token, 32768 x 6144
-  // gated: 30.3 us, there 35.9; 57344 x 8192 gated: 64 us, there 82).
+  if (m <= 16) {  // dot products: the weights' bytes, once for eight tokens
+    const double bytes = static_cast<double>((m + 7) / 8 * N * K);
+    // Above eight tokens only the smallest matrices go there, and only they are fitted.
+    least = m <= 2   ? 2.9 + bytes / 5.8e6
+            : m <= 4 ? 3.0 + bytes / 3.7e6
+            : m <= 8 ? 4.7 + bytes / 3.1e6
+                     : 3.5 + bytes / 1.2e6;
+  }
+  // Two tokens at most never go faster on the tensor cores (two tokens, 32768 x 6144
+  // gated: 32.4 us, with three there 33.9; 7168 x 7168: 9.0 and 12.7; one token, 57344
+  // x 8192 gated: 64 us, there 82).
   if (m <= 2) {
     *time = least;
     return best;
