@@ -539,6 +539,10 @@ int ar_combine_rmsnorm(const void *y, int64_t rows, const int32_t *slots,
  *
  * Streams, graph capture and ownership are those of the expert layer's calls:
  * asynchronous, no allocation, no state, device memory of the current device.
+ * That holds for the partials too: the calls over other ranks' memory
+ * (ar_rmsnorm_mapped and those of the section on cross-rank data below) end in
+ * ar_rmsnorm alone.  A group of ranks adds its partials up first and gives each
+ * rank the sum as its one partial.
  * No output may overlap an input or another output (AR_ERR_ALIAS), but
  * residual_out may be residual.  m == 0 is a no-op that checks only the sizes
  * and the options.  Inference only.
@@ -559,8 +563,10 @@ int ar_combine_rmsnorm(const void *y, int64_t rows, const int32_t *slots,
  *   out = r * rsqrt(mean(r^2) + eps) * (weight + weight_offset)
  * all in fp32 with one rounding to out's type: the norm after a block, its
  * gate and scale, the residual add and the norm before the next block in one
- * pass.  With neither post_weight, gate, scales nor offset it is ar_rmsnorm.
- * The pages have no counterpart of it.
+ * pass.  With neither post_weight, gate, scales nor offset residual_out is
+ * ar_rmsnorm's to the bit; out may differ from ar_rmsnorm's by a step, for the
+ * squares are summed in another order.  A finite row whose mean square passes
+ * fp32's range has a norm of 0.  The pages have no counterpart of it.
  *   partials       n arrays [m, H] of `type`, AR_TYPE_BF16 or AR_TYPE_F16;
  *                  n, H and eps as in ar_rmsnorm.
  *   post_weight    [H] of `type`, or NULL.    weight  [H] of `type`.
