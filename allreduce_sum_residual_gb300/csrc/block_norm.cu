@@ -13,7 +13,7 @@ static cudaError_t allow_wide_clusters(BlockNormKernel kern) {
 // Packs of a thread where there are rows enough for a CTA each.  A norm after the
 // block is a second sum that a row has to wait for: four packs a thread, half as
 // many warps to meet and more loads under way in each (8192 rows of 6144, one
-// partial: 60.5 us, with two packs 79 us).  Without it, and with so many
+// partial: 61.4 us, with two packs 79 us).  Without it, and with so many
 // partials that loads are under way anyway, two packs keep more threads (4096
 // rows of 8192: four partials and the norm 69 us against 74 us, two without it
 // 59 us against 66 us).

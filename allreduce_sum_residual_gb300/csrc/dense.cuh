@@ -1,6 +1,5 @@
 // Pieces shared by the calls of a dense layer in 8 bits (block_norm,
-// i8_quantize, i8_matmul): 16-bit packs of either type, 8-bit rounding, and
-// the host's checks of floats.
+// i8_quantize, i8_matmul): 16-bit packs of either type and 8-bit rounding.
 #pragma once
 
 #include <cuda_fp16.h>
