@@ -627,14 +627,15 @@ int ar_i8_quantize(const void *x, int type, int64_t row_stride, int64_t m,
  *
  * The sum is taken to fp32 with one rounding, and a row's results do not depend
  * on the batch it is in, while the sums on the way to it stay within 2^24: for
- * any data up to K = 1024, and at any K for data whose products have both signs
- * (a sum of K of them grows with the root of K).  Beyond that it is so for m <= 2
- * alone.  With more rows the sum is kept in fp32, to which 16 products at a time
- * are added, each time within a step (2^-23 of the sum): what comes out is off by
- * at most K / 16 + 8 steps of the largest sum on the way, however small the last
- * one is, and by how much may depend on m.  Where the operands' biases make such
- * sums, take them out of the bytes, or give AR_ACT_NONE parts of K and add the
- * outputs.  Equal calls give equal bits whatever the data.
+ * any data up to K = 1024, and at any K in practice where the products vary in
+ * sign as a layer's do (a sum of K of them then grows with the root of K: 2e6 for
+ * bytes spread evenly over all values at AR_I8_MAX_K).  Beyond that it is so for
+ * m <= 2 alone.  With more rows the sum is kept in fp32, to which 16 products at
+ * a time are added, each time within a step (2^-23 of the sum): what comes out is
+ * off by at most K / 16 + 8 steps of the largest sum on the way, however small
+ * the last one is, and by how much may depend on m.  Where an offset in both
+ * operands makes such sums, take it out of the bytes, or multiply parts of K with
+ * AR_ACT_NONE and add the outputs.  Equal calls give equal bits whatever the data.
  *
  *   x         [m, K] bytes in [-128, 127].    x_scales  [m] fp32.
  *   w         [N, K] bytes in [-128, 127].    w_scales  [N] fp32.
